@@ -1,6 +1,7 @@
 """Exact causal / non-causal attention forward on sm_103a (GB300).
 
-Thin ctypes binding over the C ABI in ``include/attn.h``: it checks and marshals
+Thin ctypes binding over the C ABI in ``include/attn.h`` and, for the paged cache's
+operators, ``include/attn_cache.h``: it checks and marshals
 torch tensors into pointers and sizes and calls the library; every step of the
 computation runs in the library's CUDA kernels.  There is no fallback: if the
 shared library is missing or the device is not sm_103, calls raise.
@@ -13,7 +14,8 @@ import os
 import threading
 
 __all__ = ["attn_fwd", "attn_fwd_into", "attn_fwd_gqa", "attn_fwd_splitkv", "splitkv_workspace_bytes",
-           "splitkv_default_splits", "row_softmax", "decode_paged", "paged_append", "load_library", "device_status", "watchdog_selftest", "AttnError",
+           "splitkv_default_splits", "row_softmax", "decode_paged", "paged_append", "prefill_paged",
+           "prefill_workspace_bytes", "paged_append_chunk", "paged_attn_mass", "paged_evict", "load_library", "device_status", "watchdog_selftest", "AttnError",
            "STATUS"]
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libeca_attn.so")
@@ -62,6 +64,25 @@ SIGNATURES = {
 }
 
 
+# The same for include/attn_cache.h.
+_PAGES = [_I] * 4  # D, page_size, max_pages, num_pages
+_FORM = [_F, _F, _I, _VP, _VP]  # scale, softcap, window, alibi_slopes, prefix_lens
+_PREFILL = [_VP] * 7 + [_I] * 4 + _PAGES + _FORM + [_VP, _SZ, _VP]
+_MASS = [_VP] * 7 + [_I] * 5 + _PAGES + _FORM + [_VP]
+_DECODE_FORM = [_VP] * 6 + [_I] * 3 + _PAGES + _FORM + [_I, _VP, _SZ, _VP]
+CACHE_SIGNATURES = {
+    "attn_prefill_paged": (_I, _PREFILL),
+    "attn_prefill_paged_bf16": (_I, _PREFILL),
+    "attn_prefill_workspace_bytes": (_SZ, [_I] * 7),
+    "attn_paged_append_chunk": (_I, [_VP] * 5 + [_I] * 3 + _PAGES + [_VP]),
+    "attn_paged_mass": (_I, _MASS),
+    "attn_paged_mass_bf16": (_I, _MASS),
+    "attn_paged_evict": (_I, [_VP] * 7 + [_I] * 2 + _PAGES + [_I, _I, _VP]),
+    "attn_decode_paged_form": (_I, _DECODE_FORM),
+    "attn_decode_paged_form_bf16": (_I, _DECODE_FORM),
+}
+
+
 class AttnError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -89,7 +110,7 @@ def load_library(path: str | None = None):
                 raise RuntimeError(f"CUDA library not built: {p} is missing "
                                    "(run python -c 'import __graft_entry__ as g; g.build()')")
             lib = ctypes.CDLL(p)
-            for name, (res, args) in SIGNATURES.items():
+            for name, (res, args) in [*SIGNATURES.items(), *CACHE_SIGNATURES.items()]:
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
@@ -308,10 +329,86 @@ def row_softmax(x, out=None, stream=None):
     return out
 
 
+def _check_cache(cache, block_table, lengths, B: int):
+    """Checks a paged cache with its table and lengths; returns (P, T, Hkv, D, max_pages)."""
+    import torch
+
+    if cache.dim() != 5 or cache.shape[1] != 2 or cache.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("cache must be [P, 2, T, Hkv, D] float16 or bfloat16")
+    if block_table.dim() != 2 or block_table.shape[0] != B or lengths.shape != (B,):
+        raise ValueError("block_table must be [B, max_pages] and lengths [B]")
+    if block_table.dtype != torch.int32 or lengths.dtype != torch.int32:
+        raise ValueError("block_table and lengths must be int32")
+    dev = cache.get_device()
+    if dev < 0 or block_table.get_device() != dev or lengths.get_device() != dev:
+        raise ValueError("cache, block_table and lengths must be CUDA tensors on one device")
+    if not (cache.is_contiguous() and block_table.is_contiguous() and lengths.is_contiguous()):
+        raise ValueError("cache, block_table and lengths must be contiguous")
+    P, _, T, Hkv, D = cache.shape
+    return P, T, Hkv, D, block_table.shape[1]
+
+
+def _check_like(name: str, t, shape, dtype, dev: int) -> None:
+    """``t`` is a contiguous tensor of this shape and dtype on CUDA device ``dev``."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
+
+
+def _form_ptrs(alibi_slopes, prefix_lens, Hq: int, B: int, dev: int):
+    """Pointers of the optional per-head slopes [Hq] and per-request prefixes [B]."""
+    import torch
+
+    slopes = prefix = None
+    if alibi_slopes is not None:
+        _check_like("alibi_slopes", alibi_slopes, (Hq,), torch.float32, dev)
+        slopes = alibi_slopes.data_ptr()
+    if prefix_lens is not None:
+        _check_like("prefix_lens", prefix_lens, (B,), torch.int32, dev)
+        prefix = prefix_lens.data_ptr()
+    return slopes, prefix
+
+
+def _workspace(workspace, need: int, dev: int):
+    """(pointer, bytes) of the caller's workspace, or of a new 256-byte aligned one, and
+    the tensor that holds it."""
+    import torch
+
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need + 256, dtype=torch.uint8, device=f"cuda:{dev}")
+        ptr = workspace.data_ptr()
+        return ptr + (-ptr) % 256, need, workspace
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+class _on_device:
+    """``torch.cuda.device(dev)`` that costs nothing when ``dev`` is current already."""
+
+    def __init__(self, dev: int):
+        import torch
+
+        self.guard = None if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
 def decode_paged(q, cache, block_table, lengths, scale: float | None = None, kv_splits: int | None = None,
-                 out=None, lse=None, workspace=None, stream=None):
+                 out=None, lse=None, workspace=None, stream=None, softcap: float = 0.0, alibi_slopes=None,
+                 window: int = 0, prefix_lens=None):
     """One decode step over a paged cache: q [B,Hq,D], cache [P,2,T,Hkv,D] (16-bit),
-    block_table [B,max_pages] int32, lengths [B] int32 (all CUDA).  Returns (out, lse)."""
+    block_table [B,max_pages] int32, lengths [B] int32 (all CUDA).  Scores may be capped
+    (``softcap``: cap * tanh(s / cap)), biased by distance (``alibi_slopes`` [Hq] float32) and
+    limited to the last ``window`` tokens, with the first ``prefix_lens`` [B] int32 tokens
+    visible whatever the window.  Returns (out, lse)."""
     import torch
 
     B, Hq, D = q.shape
@@ -325,7 +422,11 @@ def decode_paged(q, cache, block_table, lengths, scale: float | None = None, kv_
             raise ValueError("all tensors must be contiguous CUDA tensors")
     max_pages = block_table.shape[1]
     lib = load_library()
-    with torch.cuda.device(q.device):
+    dev = q.get_device()
+    form = softcap != 0.0 or window != 0 or alibi_slopes is not None or prefix_lens is not None
+    if form:
+        slopes, prefix = _form_ptrs(alibi_slopes, prefix_lens, Hq, B, dev)
+    with _on_device(dev):
         if kv_splits is None:
             kv_splits = lib.attn_decode_default_splits(B, Hq, Hkv, T, max_pages)
             if kv_splits < 0:
@@ -341,14 +442,163 @@ def decode_paged(q, cache, block_table, lengths, scale: float | None = None, kv_
             workspace = raw[off:off + need]
         if scale is None:
             scale = 1.0 / math.sqrt(D)
-        fn = lib.attn_decode_paged_bf16 if q.dtype == torch.bfloat16 else lib.attn_decode_paged
-        rc = fn(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), out.data_ptr(),
-                lse.data_ptr() if lse is not None else None, B, Hq, Hkv, D, T, max_pages, P, float(scale),
-                int(kv_splits), workspace.data_ptr() if workspace is not None else None,
-                (workspace.numel() if workspace is not None else 0), _stream_handle(stream))
+        sizes = (q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), out.data_ptr(),
+                 lse.data_ptr() if lse is not None else None, B, Hq, Hkv, D, T, max_pages, P, float(scale))
+        rest = (int(kv_splits), workspace.data_ptr() if workspace is not None else None,
+                (workspace.numel() if workspace is not None else 0), _raw_stream(dev, stream))
+        if form:
+            fn = lib.attn_decode_paged_form_bf16 if q.dtype == torch.bfloat16 else lib.attn_decode_paged_form
+            rc = fn(*sizes, float(softcap), int(window), slopes, prefix, *rest)
+        else:
+            fn = lib.attn_decode_paged_bf16 if q.dtype == torch.bfloat16 else lib.attn_decode_paged
+            rc = fn(*sizes, *rest)
     if rc != 0:
         raise AttnError(rc, "attn_decode_paged")
     return out, lse
+
+
+def prefill_workspace_bytes(total_q: int, B: int, Hq: int, Hkv: int, D: int, page_size: int, max_pages: int) -> int:
+    """Workspace bytes prefill_paged needs (0 for invalid sizes)."""
+    return int(load_library().attn_prefill_workspace_bytes(total_q, B, Hq, Hkv, D, page_size, max_pages))
+
+
+def prefill_paged(q, cache, block_table, lengths, q_offsets, scale: float | None = None, softcap: float = 0.0,
+                  alibi_slopes=None, window: int = 0, prefix_lens=None, out=None, lse=None, workspace=None,
+                  stream=None):
+    """Attention of a ragged chunk of new tokens over a paged cache that already holds their
+    K and V: q [total,Hq,D] packed, request b's rows q_offsets[b] .. q_offsets[b+1] - 1 (q_offsets
+    [B+1] int32) the last of its lengths[b] tokens; causal; score forms as in decode_paged
+    (prefix_lens tokens are visible to every row, earlier ones too).  Rows past q_offsets[B] are
+    left alone.  Returns (out, lse [total,Hq] float32)."""
+    import torch
+
+    total, Hq, D = q.shape
+    B = lengths.shape[0]
+    P, T, Hkv, D2, max_pages = _check_cache(cache, block_table, lengths, B)
+    dev = cache.get_device()
+    dt = cache.dtype
+    if D2 != D:
+        raise ValueError("q and cache must have the same head size")
+    _check_like("q", q, (total, Hq, D), dt, dev)
+    _check_like("q_offsets", q_offsets, (B + 1,), torch.int32, dev)
+    slopes, prefix = _form_ptrs(alibi_slopes, prefix_lens, Hq, B, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_like("out", out, (total, Hq, D), dt, dev)
+    if lse is None:
+        lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _check_like("lse", lse, (total, Hq), torch.float32, dev)
+    lib = load_library()
+    need = 0 if workspace is not None else lib.attn_prefill_workspace_bytes(total, B, Hq, Hkv, D, T, max_pages)
+    ws, ws_bytes, held = _workspace(workspace, need, dev)
+    fn = lib.attn_prefill_paged_bf16 if dt == torch.bfloat16 else lib.attn_prefill_paged
+    with _on_device(dev):
+        rc = fn(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), q_offsets.data_ptr(),
+                out.data_ptr(), lse.data_ptr(), total, B, Hq, Hkv, D, T, max_pages, P,
+                1.0 / math.sqrt(D) if scale is None else float(scale), float(softcap), int(window), slopes, prefix,
+                ws, ws_bytes, _raw_stream(dev, stream))
+    if rc != 0:
+        raise AttnError(rc, "attn_prefill_paged")
+    return out, lse
+
+
+def paged_append_chunk(new_kv, cache, block_table, lengths, q_offsets, stream=None) -> None:
+    """Write new_kv [total, 2, Hkv, D], a ragged chunk packed as for prefill_paged, to the last
+    positions of every request: its i-th row to lengths[b] - n_b + i."""
+    import torch
+
+    B = lengths.shape[0]
+    P, T, Hkv, D, max_pages = _check_cache(cache, block_table, lengths, B)
+    dev = cache.get_device()
+    total = new_kv.shape[0]
+    _check_like("new_kv", new_kv, (total, 2, Hkv, D), cache.dtype, dev)
+    _check_like("q_offsets", q_offsets, (B + 1,), torch.int32, dev)
+    with _on_device(dev):
+        rc = load_library().attn_paged_append_chunk(
+            new_kv.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), q_offsets.data_ptr(),
+            total, B, Hkv, D, T, max_pages, P, _raw_stream(dev, stream))
+    if rc != 0:
+        raise AttnError(rc, "attn_paged_append_chunk")
+
+
+def paged_attn_mass(q, lse, cache, block_table, lengths, q_offsets=None, mass=None, scale: float | None = None,
+                    softcap: float = 0.0, alibi_slopes=None, window: int = 0, prefix_lens=None, stream=None):
+    """The attention weight every cached token received from the rows of q [total,Hq,D] (packed as
+    for prefill_paged, or one row a request when q_offsets is None), whose log-sum-exps lse
+    [total,Hq] came from prefill_paged or decode_paged with the same score form: summed over the
+    rows and the query heads of each key/value head.  Added to ``mass`` [B,Hkv,max_pages*T] float32
+    when given, else written to a new one.  Returns mass."""
+    import torch
+
+    total, Hq, D = q.shape
+    B = lengths.shape[0]
+    P, T, Hkv, D2, max_pages = _check_cache(cache, block_table, lengths, B)
+    dev = cache.get_device()
+    dt = cache.dtype
+    if D2 != D:
+        raise ValueError("q and cache must have the same head size")
+    _check_like("q", q, (total, Hq, D), dt, dev)
+    _check_like("lse", lse, (total, Hq), torch.float32, dev)
+    offsets = None
+    if q_offsets is not None:
+        _check_like("q_offsets", q_offsets, (B + 1,), torch.int32, dev)
+        offsets = q_offsets.data_ptr()
+    elif total != B:
+        raise ValueError("without q_offsets q holds one row a request")
+    slopes, prefix = _form_ptrs(alibi_slopes, prefix_lens, Hq, B, dev)
+    accumulate = mass is not None
+    if accumulate:
+        _check_like("mass", mass, (B, Hkv, max_pages * T), torch.float32, dev)
+    else:
+        mass = torch.empty((B, Hkv, max_pages * T), dtype=torch.float32, device=q.device)
+    lib = load_library()
+    fn = lib.attn_paged_mass_bf16 if dt == torch.bfloat16 else lib.attn_paged_mass
+    with _on_device(dev):
+        rc = fn(q.data_ptr(), lse.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), offsets,
+                mass.data_ptr(), int(accumulate), total, B, Hq, Hkv, D, T, max_pages, P,
+                1.0 / math.sqrt(D) if scale is None else float(scale), float(softcap), int(window), slopes, prefix,
+                _raw_stream(dev, stream))
+    if rc != 0:
+        raise AttnError(rc, "attn_paged_mass")
+    return mass
+
+
+def paged_evict(cache, block_table, lengths, mass, budget: int, recent: int = 0, kept=None, new_lengths=None,
+                mass_out=None, stream=None):
+    """Shrink every request that holds more than ``budget`` tokens to ``budget`` of them, per
+    key/value head: the last ``recent`` tokens and, of the others, those with the largest mass
+    [B,Hkv,max_pages*T] float32 (ties: the lowest position).  Their rows move in place to positions
+    0 .. budget - 1, in order.  Returns (kept [B,Hkv,budget] int32: each one's old position, then
+    -1; new_lengths [B] int32; mass_out: the kept tokens' mass, then 0)."""
+    import torch
+
+    B = lengths.shape[0]
+    P, T, Hkv, D, max_pages = _check_cache(cache, block_table, lengths, B)
+    dev = cache.get_device()
+    _check_like("mass", mass, (B, Hkv, max_pages * T), torch.float32, dev)
+    budget = int(budget)
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=cache.device)
+    else:
+        _check_like("kept", kept, (B, Hkv, budget), torch.int32, dev)
+    if new_lengths is None:
+        new_lengths = torch.empty_like(lengths)
+    else:
+        _check_like("new_lengths", new_lengths, (B,), torch.int32, dev)
+    if mass_out is None:
+        mass_out = torch.empty_like(mass)
+    else:
+        _check_like("mass_out", mass_out, (B, Hkv, max_pages * T), torch.float32, dev)
+    with _on_device(dev):
+        rc = load_library().attn_paged_evict(
+            cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), mass.data_ptr(), kept.data_ptr(),
+            new_lengths.data_ptr(), mass_out.data_ptr(), B, Hkv, D, T, max_pages, P, budget, int(recent),
+            _raw_stream(dev, stream))
+    if rc != 0:
+        raise AttnError(rc, "attn_paged_evict")
+    return kept, new_lengths, mass_out
 
 
 def paged_append(new_kv, cache, block_table, lengths, stream=None) -> None:

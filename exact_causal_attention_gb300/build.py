@@ -1,4 +1,4 @@
-"""Builds the CUDA library in-tree: one nvcc invocation, sm_103a only."""
+"""Builds the CUDA library in-tree with nvcc, sm_103a only."""
 from __future__ import annotations
 
 import os
@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 # The same sources with ECA_ANATOMY: the attention kernel records per-CTA milestone
 # stamps (a measurement aid; nothing else changes).
 ANATOMY_LIB_PATH = os.path.join(BUILD_DIR, "libeca_attn_anatomy.so")
-SOURCES = ["attn_api.cu"]
+SOURCES = ["attn_api.cu", "cache_api.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -25,37 +25,57 @@ def _nvcc() -> str:
 
 
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))]
-    files.append(os.path.join(INCLUDE, "attn.h"))
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return files
 
 
-def _command(out: str, defines, verbose: bool):
-    cuda_lib = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "lib64")
-    cmd = [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "--shared", "-Xcompiler", "-fPIC",
-           "-cudart", "shared", "-I", INCLUDE, "-I", CSRC, "-Xlinker", f"-rpath,{cuda_lib}", *defines,
-           "-o", out, *[os.path.join(CSRC, s) for s in SOURCES]]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    return cmd
+def _flags(verbose: bool):
+    return [*ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-cudart", "shared", "-I", INCLUDE,
+            "-I", CSRC, *(["-Xptxas=-v"] if verbose else [])]
+
+
+def _run(commands):
+    """Run all commands at once; raise when one fails."""
+    procs = [(subprocess.Popen(cmd), cmd) for cmd in commands]
+    failed = [cmd for proc, cmd in procs if proc.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(1, " ".join(failed[0]))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/ into _build/libeca_attn.so (and the anatomy variant beside it, in
-    parallel) unless both are newer than every source.  Returns the main library."""
+    """Compile csrc/ into _build/libeca_attn.so (and the anatomy variant beside it; all
+    translation units in parallel) unless both are newer than every source.  Returns the
+    main library."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     newest = max(os.path.getmtime(f) for f in _deps())
-    todo = [(path, defines) for path, defines in ((LIB_PATH, []), (ANATOMY_LIB_PATH, ["-DECA_ANATOMY"]))
-            if force or not os.path.exists(path) or os.path.getmtime(path) < newest]
-    procs = []
-    for path, defines in todo:
-        tmp = path + f".tmp{os.getpid()}"
-        procs.append((subprocess.Popen(_command(tmp, defines, verbose)), tmp, path))
-    failed = [path for proc, _, path in procs if proc.wait() != 0]
-    if failed:
-        raise subprocess.CalledProcessError(1, f"nvcc for {failed}")
-    for _, tmp, path in procs:
-        os.replace(tmp, path)
+    libs = [(LIB_PATH, []), (ANATOMY_LIB_PATH, ["-DECA_ANATOMY"])]
+    if not force and all(os.path.exists(path) and os.path.getmtime(path) >= newest for path, _ in libs):
+        return LIB_PATH
+    cuda_lib = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "lib64")
+    tag = f".tmp{os.getpid()}"
+    objects, compiles, links = [], [], []
+    for path, defines in libs:
+        mine = []
+        for source in SOURCES:
+            # Only the first source holds the attention kernel that the define changes.
+            variant = os.path.basename(path) if source == SOURCES[0] else "shared"
+            obj = os.path.join(BUILD_DIR, f"{source}.{variant}{tag}.o")
+            if obj not in objects:
+                objects.append(obj)
+                compiles.append([_nvcc(), *_flags(verbose), *defines, "-c", os.path.join(CSRC, source), "-o", obj])
+            mine.append(obj)
+        links.append([_nvcc(), *ARCH_FLAGS, "--shared", "-cudart", "shared", "-Xlinker", f"-rpath,{cuda_lib}",
+                      "-o", path + tag, *mine])
+    try:
+        _run(compiles)
+        _run(links)
+        for path, _ in libs:
+            os.replace(path + tag, path)
+    finally:
+        for f in [*objects, *(path + tag for path, _ in libs)]:
+            if os.path.exists(f):
+                os.remove(f)
     return LIB_PATH
 
 

@@ -10,11 +10,14 @@
 #include <functional>
 #include <mutex>
 #include <queue>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
 #include "attn.h"
+#include "attn_cache.h"
 #include "attn_fwd_kernel.cuh"
+#include "host_common.h"
 #include "paged_decode.cuh"
 #include "row_softmax.cuh"
 #include "splitkv_combine.cuh"
@@ -29,7 +32,8 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr int kMaxSplits = 64;
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s per single wait
+using eca_host::kWaitLimitNs;
+using eca_host::launch_pdl;
 
 // Device status word: 0, or the code of the last bounded wait that gave up.
 __device__ int g_device_status = 0;
@@ -230,13 +234,10 @@ int cached_qkv_map(MapCache& cache, EncodeTiledFn encode, CUtensorMap* map, cons
   return rc;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Do [a, a + na) and [b, b + nb) intersect?
-bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
+using eca_host::align256;
+using eca_host::aligned;
+using eca_host::check_paged_args;
+using eca_host::overlaps;
 
 // Checks that need no GPU.  Order: pointers, sizes, head dim, scale, alignment, overlap.
 int check_args(const void* q, const void* k, const void* v, const void* o, const float* lse, int B,
@@ -365,39 +366,6 @@ int predicted_best_splits(int B, int H, int N, int D, int sm_count) {
     }
   }
   return best;
-}
-
-uint64_t align256(uint64_t x) { return (x + 255) & ~static_cast<uint64_t>(255); }
-
-// Launch with programmatic stream serialisation: the grid may be scheduled before
-// the grid ahead of it on the stream has finished.  Only kernels that call
-// grid_dependency_wait before touching global memory are launched this way.
-// Between two back-to-back attention launches the second then starts as soon as
-// the first completes, instead of after the full stream-ordered launch latency.
-// ECA_PDL=0 in the environment (read once per process) launches in plain stream
-// order instead, with the same results; it exists to measure the difference.
-bool programmatic_launch_enabled() {
-  static const bool enabled = [] {
-    const char* v = std::getenv("ECA_PDL");
-    return !(v != nullptr && v[0] == '0' && v[1] == '\0');
-  }();
-  return enabled;
-}
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
-                       Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = programmatic_launch_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 // Workspace of a key split: fp32 partial outputs [splits, BH, N, D], then fp32
@@ -633,28 +601,13 @@ int encode_cache_map(EncodeTiledFn encode, CUtensorMap* map, const void* cache, 
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
-int check_paged_args(const void* cache, const int* block_table, const int* lengths, int B, int Hkv, int D,
-                     int page_size, int max_pages, int num_pages) {
-  if (!cache || !block_table || !lengths) return ATTN_ERR_INVALID_ARG;
-  if (B < 1 || Hkv < 1 || max_pages < 1 || num_pages < 1) return ATTN_ERR_INVALID_ARG;
-  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED_D;
-  if (page_size != 8 && page_size != 16 && page_size != 32 && page_size != 64) return ATTN_ERR_INVALID_ARG;
-  if (!aligned(cache, 16) || !aligned(block_table, 4) || !aligned(lengths, 4)) return ATTN_ERR_UNALIGNED;
-  // The decode kernel addresses the cache's (page, kind, token) rows with a signed 32-bit tensor
-  // coordinate, so there must be fewer than 2^31 of them.
-  const uint64_t rows = static_cast<uint64_t>(num_pages) * 2 * static_cast<uint64_t>(page_size);
-  if (rows > 0x7fffffffull || static_cast<uint64_t>(max_pages) * page_size > 0x7fffffffull) return ATTN_ERR_INVALID_ARG;
-  if (static_cast<uint64_t>(B) * static_cast<uint64_t>(max_pages) > 0x7fffffffull) return ATTN_ERR_INVALID_ARG;
-  return ATTN_OK;
-}
-
 uint64_t decode_ws_bytes(uint64_t B, uint64_t Hq, uint64_t D, uint64_t splits, uint64_t* lse_off) {
   const uint64_t o = splits * B * Hq * D * 4;
   if (lse_off) *lse_off = align256(o);
   return align256(o) + align256(splits * B * Hq * 4);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool FORM>
 int launch_decode(const CUtensorMap& tm, eca::DecodeParams& p, const DecodeShape& sh, DeviceState* st,
                   cudaStream_t stream) {
   using L = eca::DecodeSmem<D>;
@@ -677,18 +630,18 @@ int launch_decode(const CUtensorMap& tm, eca::DecodeParams& p, const DecodeShape
     }
     return ATTN_OK;
   };
-  const unsigned base = (D == 128 ? 0u : 8u) + (BF16 ? 4u : 0u);
+  const unsigned base = (D == 128 ? 0u : 8u) + (BF16 ? 4u : 0u) + (FORM ? 16u : 0u);
   int rc;
   switch (sh.hc) {
-    case 8: rc = run(eca::paged_decode_kernel<D, BF16, 8>, 1u << (base + 3)); break;
-    case 4: rc = run(eca::paged_decode_kernel<D, BF16, 4>, 1u << (base + 2)); break;
-    case 2: rc = run(eca::paged_decode_kernel<D, BF16, 2>, 1u << (base + 1)); break;
-    default: rc = run(eca::paged_decode_kernel<D, BF16, 1>, 1u << base); break;
+    case 8: rc = run(eca::paged_decode_kernel<D, BF16, 8, FORM>, 1u << (base + 3)); break;
+    case 4: rc = run(eca::paged_decode_kernel<D, BF16, 4, FORM>, 1u << (base + 2)); break;
+    case 2: rc = run(eca::paged_decode_kernel<D, BF16, 2, FORM>, 1u << (base + 1)); break;
+    default: rc = run(eca::paged_decode_kernel<D, BF16, 1, FORM>, 1u << base); break;
   }
   if (rc != ATTN_OK || p.part_o == nullptr || p.counters != nullptr) return rc;  // merged in the kernel
   const long long rows = static_cast<long long>(p.B) * p.Hq;
   const long long want = (rows + 7) / 8, cap = static_cast<long long>(st->sm_count) * 8;
-  if (launch_pdl(eca::paged_decode_combine<D, BF16>, static_cast<unsigned>(want < cap ? want : cap), 256, 0, stream,
+  if (launch_pdl(eca::paged_decode_combine<D, BF16, FORM>, static_cast<unsigned>(want < cap ? want : cap), 256, 0, stream,
                  p) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_LAUNCH;
@@ -698,13 +651,16 @@ int launch_decode(const CUtensorMap& tm, eca::DecodeParams& p, const DecodeShape
 
 int decode_impl(bool bf16, const void* q, const void* cache, const int* block_table, const int* lengths, void* out,
                 float* lse, int B, int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages, float scale,
-                int kv_splits, void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+                int kv_splits, void* workspace, size_t workspace_bytes, attn_stream_t stream, float softcap = 0.f,
+                int window = 0, const float* slopes = nullptr, const int* prefix = nullptr) {
   int rc = check_paged_args(cache, block_table, lengths, B, Hkv, D, page_size, max_pages, num_pages);
   if (rc != ATTN_OK) return rc;
   if (!q || !out || Hq < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   if (kv_splits < 1 || kv_splits > kMaxSplits) return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4))) return ATTN_ERR_UNALIGNED;
+  if (!std::isfinite(softcap) || softcap < 0.f || window < 0) return ATTN_ERR_INVALID_ARG;
+  if ((slopes && !aligned(slopes, 4)) || (prefix && !aligned(prefix, 4))) return ATTN_ERR_UNALIGNED;
   const uint64_t qbytes = static_cast<uint64_t>(B) * Hq * D * 2;
   if (overlaps(out, qbytes, q, qbytes)) return ATTN_ERR_INVALID_ARG;
   const DecodeShape sh = decode_shape(Hq, Hkv, page_size, max_pages, kv_splits);
@@ -753,6 +709,13 @@ int decode_impl(bool bf16, const void* q, const void* cache, const int* block_ta
   p.timeout_code = ATTN_ERR_TIMEOUT;
   p.bad_index_code = ATTN_ERR_BAD_INDEX;
   p.counters = nullptr;
+  p.softcap = softcap;
+  p.scale = softcap > 0.f ? scale / softcap : scale;
+  p.slopes = slopes;
+  p.prefix = prefix;
+  p.window = window;
+  // A prefix changes nothing where every token is visible.
+  const bool form = softcap > 0.f || window > 0 || slopes != nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const long long groups = static_cast<long long>(B) * Hkv * sh.head_chunks;
   unsigned slot = 0;
@@ -762,16 +725,87 @@ int decode_impl(bool bf16, const void* q, const void* cache, const int* block_ta
     if (rc != ATTN_OK) return rc;
     p.counters = st->dec_counters + static_cast<size_t>(slot) * kDecCountersPerSlot;
   }
-  if (D == 128) {
-    rc = bf16 ? launch_decode<128, true>(tm, p, sh, st, s) : launch_decode<128, false>(tm, p, sh, st, s);
-  } else {
-    rc = bf16 ? launch_decode<64, true>(tm, p, sh, st, s) : launch_decode<64, false>(tm, p, sh, st, s);
-  }
+  auto launch = [&](auto with_form) -> int {
+    constexpr bool kForm = decltype(with_form)::value;
+    if (D == 128) {
+      return bf16 ? launch_decode<128, true, kForm>(tm, p, sh, st, s) : launch_decode<128, false, kForm>(tm, p, sh, st, s);
+    }
+    return bf16 ? launch_decode<64, true, kForm>(tm, p, sh, st, s) : launch_decode<64, false, kForm>(tm, p, sh, st, s);
+  };
+  rc = form ? launch(std::true_type{}) : launch(std::false_type{});
   if (rc != ATTN_OK || p.counters == nullptr) return rc;
   return st->dec_slots.release(s, slot, capturing);
 }
 
 }  // namespace
+
+namespace eca_host {
+
+int current_device(Device* out) {
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != ATTN_OK) return rc;
+  *out = Device{static_cast<int>(st - g_devices), st->sm_count, st->status};
+  return ATTN_OK;
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+uint64_t align256(uint64_t x) { return (x + 255) & ~static_cast<uint64_t>(255); }
+
+bool programmatic_launch_enabled() {
+  static const bool enabled = [] {
+    const char* v = std::getenv("ECA_PDL");
+    return !(v != nullptr && v[0] == '0' && v[1] == '\0');
+  }();
+  return enabled;
+}
+
+int check_paged_args(const void* cache, const int* block_table, const int* lengths, int B, int Hkv, int D,
+                     int page_size, int max_pages, int num_pages) {
+  if (!cache || !block_table || !lengths) return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || max_pages < 1 || num_pages < 1) return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED_D;
+  if (page_size != 8 && page_size != 16 && page_size != 32 && page_size != 64) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(cache, 16) || !aligned(block_table, 4) || !aligned(lengths, 4)) return ATTN_ERR_UNALIGNED;
+  // The decode kernel addresses the cache's (page, kind, token) rows with a signed 32-bit tensor
+  // coordinate, so there must be fewer than 2^31 of them.
+  const uint64_t rows = static_cast<uint64_t>(num_pages) * 2 * static_cast<uint64_t>(page_size);
+  if (rows > 0x7fffffffull || static_cast<uint64_t>(max_pages) * page_size > 0x7fffffffull) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<uint64_t>(B) * static_cast<uint64_t>(max_pages) > 0x7fffffffull) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+int paged_cache_map(CUtensorMap* map, const void* cache, bool bf16, int D, int Hkv, int T, int P) {
+  std::lock_guard<std::mutex> lock(g_mutex);
+  EncodeTiledFn encode = nullptr;
+  const int rc = get_encode_fn(&encode);
+  return rc != ATTN_OK ? rc : encode_cache_map(encode, map, cache, bf16, D, Hkv, T, P);
+}
+
+int head_rows_map(CUtensorMap* map, const void* ptr, bool bf16, int D, int H, int R, unsigned box_h, unsigned box_r) {
+  std::lock_guard<std::mutex> lock(g_mutex);
+  EncodeTiledFn encode = nullptr;
+  const int rc = get_encode_fn(&encode);
+  if (rc != ATTN_OK) return rc;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(R)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(H) * D * 2};
+  const cuuint32_t box[3] = {64, box_h, box_r};
+  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  const CUresult r =
+      encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(ptr), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+}  // namespace eca_host
 
 extern "C" {
 
@@ -868,6 +902,23 @@ int attn_decode_paged_bf16(const void* q, const void* cache, const int* block_ta
                            attn_stream_t stream) {
   return decode_impl(true, q, cache, block_table, lengths, out, lse, B, Hq, Hkv, D, page_size, max_pages, num_pages,
                      scale, kv_splits, workspace, workspace_bytes, stream);
+}
+
+int attn_decode_paged_form(const void* q, const void* cache, const int* block_table, const int* lengths, void* out,
+                           float* lse, int B, int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages,
+                           float scale, float softcap, int window, const float* alibi_slopes, const int* prefix_lens,
+                           int kv_splits, void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  return decode_impl(false, q, cache, block_table, lengths, out, lse, B, Hq, Hkv, D, page_size, max_pages, num_pages,
+                     scale, kv_splits, workspace, workspace_bytes, stream, softcap, window, alibi_slopes, prefix_lens);
+}
+
+int attn_decode_paged_form_bf16(const void* q, const void* cache, const int* block_table, const int* lengths,
+                                void* out, float* lse, int B, int Hq, int Hkv, int D, int page_size, int max_pages,
+                                int num_pages, float scale, float softcap, int window, const float* alibi_slopes,
+                                const int* prefix_lens, int kv_splits, void* workspace, size_t workspace_bytes,
+                                attn_stream_t stream) {
+  return decode_impl(true, q, cache, block_table, lengths, out, lse, B, Hq, Hkv, D, page_size, max_pages, num_pages,
+                     scale, kv_splits, workspace, workspace_bytes, stream, softcap, window, alibi_slopes, prefix_lens);
 }
 
 size_t attn_decode_workspace_bytes(int B, int Hq, int D, int kv_splits) {

@@ -34,7 +34,7 @@
 #include <cuda.h>
 #include <cstdint>
 
-#include "ptx.cuh"
+#include "paged_common.cuh"
 
 namespace eca {
 
@@ -63,7 +63,45 @@ struct DecodeParams {
   // left zero; the last segment to finish merges the group's partial results.
   // Null: a separate merge kernel does it.
   unsigned* counters;
+  // Score forms (the FORM instances; include/attn_cache.h).
+  float softcap;        // 0: none
+  float scale;          // scale / softcap where there is a cap
+  const float* slopes;  // [Hq] or null
+  const int* prefix;    // [B] or null
+  int window;           // 0: none
 };
+
+// Visible pages of one request under the FORM instances: logical pages 0 .. pre - 1
+// (the prefix) and from pre + gap on (the window), counted without the gap.  Without
+// a window every page up to the length is visible and the gap is 0.
+struct DecodePages {
+  int n;        // visible pages
+  int pre, gap;
+  int lo;       // first token of the window
+  int prefix;   // tokens of the prefix
+  int seg_pages;  // pages of one segment: the visible pages shared out evenly, whole tiles
+  __device__ __forceinline__ int logical(int v) const { return v < pre ? v : v + gap; }
+};
+
+__device__ __forceinline__ DecodePages decode_pages(const DecodeParams& p, int b, int len, int log2T) {
+  DecodePages d;
+  d.prefix = p.prefix != nullptr ? min(max(p.prefix[b], 0), len) : 0;
+  d.lo = p.window > 0 ? max(0, len - p.window) : 0;
+  const int T = 1 << log2T;
+  const int n_pages = (len + T - 1) >> log2T;
+  d.pre = (d.prefix + T - 1) >> log2T;
+  d.gap = max(0, (d.lo >> log2T) - d.pre);
+  d.n = n_pages - d.gap;
+  const int per_tile = kDecTile >> log2T;
+  const int seg = (d.n + p.splits - 1) / p.splits;
+  d.seg_pages = max(1, (seg + per_tile - 1) / per_tile) * per_tile;
+  return d;
+}
+
+// Bits 0 .. n - 1.
+__device__ __forceinline__ unsigned long long low_bits(int n) {
+  return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1);
+}
 
 template <int D>
 struct DecodeSmem {
@@ -82,22 +120,6 @@ struct DecodeSmem {
   static_assert(kDecWarps * 8 * D * 4 <= kDecStages * kStageBytes, "reduction buffer fits over the ring");
   static_assert(kBarOff % 8 == 0, "mbarriers are 8-byte aligned");
 };
-
-template <bool BF16>
-__device__ __forceinline__ float to_f32(uint16_t h) {
-  if constexpr (BF16) {
-    return __uint_as_float(static_cast<uint32_t>(h) << 16);
-  } else {
-    float f;
-    asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(h));
-    return f;
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ float2 to_f32x2(uint32_t w) {
-  return make_float2(to_f32<BF16>(static_cast<uint16_t>(w & 0xffffu)), to_f32<BF16>(static_cast<uint16_t>(w >> 16)));
-}
 
 // Byte offset, inside one kind of a tile, of the 16-byte chunk c (0 .. D/8 - 1) of
 // token row r.  Rows are staged as swizzled (T x 64) boxes: box (page, half) holds
@@ -144,7 +166,10 @@ __device__ __forceinline__ void mma_16816(float& d0, float& d1, float& d2, float
   }
 }
 
-template <int D, bool BF16, int HC>
+// FORM: with score forms (a tanh cap, a distance bias, a window and a prefix); then the
+// segments share out each request's visible pages evenly, and a page id is read
+// only once the length is known.
+template <int D, bool BF16, int HC, bool FORM = false>
 __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUtensorMap tm_cache,
                                                                    const DecodeParams p) {
   static_assert(HC >= 1 && HC <= 8, "query heads per CTA are rows 0-7 of the padded products");
@@ -189,9 +214,9 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
   // after it (the table row holds max_pages entries, so the read stays inside it);
   // ids past the request's last page are read but never followed.
   const int* table_row = p.block_table + static_cast<size_t>(b) * p.max_pages;
-  const int pg_begin = seg * p.seg_pages;
+  int pg_begin = seg * p.seg_pages;
   int id_first = -1;
-  if (tid < kDecIdRing && pg_begin + tid < min(p.max_pages, pg_begin + p.seg_pages)) {
+  if (!FORM && tid < kDecIdRing && pg_begin + tid < min(p.max_pages, pg_begin + p.seg_pages)) {
     id_first = table_row[pg_begin + tid];
   }
   int len = p.lengths[b];
@@ -199,8 +224,17 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
     if (tid == 0) atomicExch(p.status, p.bad_index_code);
     len = len < 0 ? 0 : p.max_pages * T;
   }
-  const int n_pages = (len + T - 1) >> log2T;
-  const int pg_end = min(n_pages, pg_begin + p.seg_pages);
+  DecodePages vis = {};
+  if constexpr (FORM) {
+    vis = decode_pages(p, b, len, log2T);
+    pg_begin = seg * vis.seg_pages;
+  }
+  auto seg_pages = [&]() { return FORM ? vis.seg_pages : p.seg_pages; };
+  const int n_pages = FORM ? vis.n : (len + T - 1) >> log2T;
+  const int pg_end = min(n_pages, pg_begin + seg_pages());
+  if constexpr (FORM) {
+    if (tid < kDecIdRing && pg_begin + tid < pg_end) id_first = table_row[vis.logical(pg_begin + tid)];
+  }
   const int n_tiles = pg_end > pg_begin ? (pg_end - pg_begin + pages_per_tile - 1) / pages_per_tile : 0;
 
   if (tid == 0) {
@@ -280,8 +314,14 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
         for (int pp = 0; pp < 8; ++pp) {
           if (ids[pp] < 0) continue;
           ++good;
-          const int lo = pp << log2T, hi = min((pp + 1) << log2T, len - tok0);
-          if (hi > lo) rows_ok |= (hi - lo == 64 ? ~0ull : ((1ull << (hi - lo)) - 1)) << lo;
+          if constexpr (FORM) {
+            const int tok = vis.logical(first_page + pp) << log2T;
+            const unsigned long long seen = ~low_bits(vis.lo - tok) | low_bits(vis.prefix - tok);
+            rows_ok |= (low_bits(min(T, len - tok)) & seen) << (pp << log2T);
+          } else {
+            const int lo = pp << log2T, hi = min((pp + 1) << log2T, len - tok0);
+            if (hi > lo) rows_ok |= (hi - lo == 64 ? ~0ull : ((1ull << (hi - lo)) - 1)) << lo;
+          }
         }
         rows_s[slot] = rows_ok;
         mbar_arrive_expect_tx(full(slot), static_cast<uint32_t>(good * 2 * (D / 64) * T * 128));
@@ -303,7 +343,7 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
           const int page = pg_begin + first + pp + kDecIdRing;
           if (page < pg_end) {
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(ids_s + (first + pp) % kDecIdRing)),
-                         "l"(table_row + page)
+                         "l"(table_row + (FORM ? vis.logical(page) : page))
                          : "memory");
           }
         }
@@ -318,6 +358,11 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
   } else {
     // ------------------------------------------------------------ compute warps
     const float c = p.scale_log2e;
+    float cap2 = 0.f, slope2 = 0.f;  // cap and this head's slope in the base-2 domain
+    if constexpr (FORM) {
+      cap2 = p.softcap * 1.4426950408889634f;
+      if (p.slopes != nullptr && head < HC) slope2 = p.slopes[qh0 + head] * 1.4426950408889634f;
+    }
     const int tok_w = 16 * warp;  // this warp's rows of every tile
     for (int i = 0; i < n_tiles; ++i) {
       const int slot = i % kDecStages;
@@ -350,7 +395,15 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = tok_w + 8 * nb + 2 * (lane & 3) + e;
-          x[2 * nb + e] = ((rows_ok >> r) & 1ull) ? sacc[nb][e] * c : -INFINITY;
+          float sc = sacc[nb][e] * c;
+          if constexpr (FORM) {
+            if (p.softcap > 0.f) sc = cap2 * tanhf(sacc[nb][e] * p.scale);
+            if (p.slopes != nullptr) {
+              const int tok = (vis.logical(pg_begin + i * pages_per_tile + (r >> log2T)) << log2T) + (r & (T - 1));
+              sc -= slope2 * static_cast<float>(len - 1 - tok);
+            }
+          }
+          x[2 * nb + e] = ((rows_ok >> r) & 1ull) ? sc : -INFINITY;
         }
       }
       // online softmax over this warp's tokens: m' = max(m, max s), p = 2^(s - m'),
@@ -476,7 +529,7 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
   if (p.part_o == nullptr || p.counters == nullptr) return;
   // Merge of the segments (section 6.4, log-sum-exp form) by the group's last
   // segment to finish: lse = ln sum_s e^(lse_s), O = sum_s e^(lse_s - lse) O_s.
-  const int valid = min(p.splits, (n_pages + p.seg_pages - 1) / p.seg_pages);  // segments with pages
+  const int valid = min(p.splits, (n_pages + seg_pages() - 1) / seg_pages());  // segments with pages
   volatile int* last_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
   const size_t stride = static_cast<size_t>(p.B) * p.Hq;
   if (seg < valid) {
@@ -550,7 +603,7 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
 // Merge of the decode segments (section 6.4 of the page, in log-sum-exp form as in
 // the prefill merge): rows are (b, query head); segment s is non-empty when its
 // first logical page is below the request's page count.
-template <int D, bool BF16>
+template <int D, bool BF16, bool FORM = false>
 __global__ void __launch_bounds__(256) paged_decode_combine(const DecodeParams p) {
   grid_dependency_wait();  // the partials come from the decode grid just ahead
   const int lane = threadIdx.x % 32;
@@ -559,8 +612,14 @@ __global__ void __launch_bounds__(256) paged_decode_combine(const DecodeParams p
     const int b = static_cast<int>(r / p.Hq);
     int len = p.lengths[b];
     len = len < 0 ? 0 : (len > p.max_pages * p.page_size ? p.max_pages * p.page_size : len);
-    const int n_pages = (len + p.page_size - 1) / p.page_size;
-    const int valid = min(p.splits, (n_pages + p.seg_pages - 1) / p.seg_pages);
+    int n_pages = (len + p.page_size - 1) / p.page_size;
+    int seg_pages = p.seg_pages;
+    if constexpr (FORM) {
+      const DecodePages vis = decode_pages(p, b, len, 31 - __clz(p.page_size));
+      n_pages = vis.n;
+      seg_pages = vis.seg_pages;
+    }
+    const int valid = min(p.splits, (n_pages + seg_pages - 1) / seg_pages);
     const size_t stride = static_cast<size_t>(p.B) * p.Hq;
     float m = -INFINITY;
     for (int s = 0; s < valid; ++s) m = fmaxf(m, p.part_lse[s * stride + r]);
