@@ -1,6 +1,7 @@
 // Host side of include/attn_cache.h: argument checks and launches of the paged cache's
 // operators.  The one-token decode with score forms is in attn_api.cu, beside
 // attn_decode_paged.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -50,16 +51,88 @@ int check_chunk_args(const void* q, int total, int Hq, int Hkv, int D, float sca
   return ATTN_OK;
 }
 
+// A window that reaches past every context is none.
+eca::ScoreForm score_form(float scale, float softcap, int window, const float* slopes, const int* prefix, int most) {
+  return eca::ScoreForm{scale, softcap, slopes, prefix, window >= most ? 0 : window};
+}
+
 int launched(cudaError_t e) {
   if (e == cudaSuccess) return ATTN_OK;
   cudaGetLastError();  // clear the error the failed launch recorded
   return ATTN_ERR_LAUNCH;
 }
 
+// Shared memory and register checks of a kernel, once per device and instance.
+template <typename Kernel>
+int configure(Kernel kernel, const Device& dev, std::atomic<uint64_t>* done, int smem, int min_regs) {
+  const uint64_t bit = 1ull << dev.index;  // fewer than 64 devices
+  if (done->load(std::memory_order_acquire) & bit) return ATTN_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_ERR_CUDA;
+  }
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (fa.numRegs < min_regs) return ATTN_ERR_LAUNCH;
+  done->fetch_or(bit, std::memory_order_release);
+  return ATTN_OK;
+}
+
+// Heads of a key/value group that share a query tile: the largest divisor of the
+// group's size that fits its 128 rows.
+int heads_per_tile(int group) {
+  int hc = group < eca::kPfTile ? group : eca::kPfTile;
+  while (group % hc != 0) --hc;
+  return hc;
+}
+
+struct PrefillShape {
+  int hc, chunks, tq;
+  int grid;             // CTAs: no more than there can be work for
+  uint64_t o_bytes, lse_bytes, bytes;
+};
+
+constexpr int kPrefillMaxCtas = 160;
+
+PrefillShape prefill_shape(int total_q, int B, int Hq, int Hkv, int D, int page_size, int max_pages) {
+  PrefillShape sh;
+  const int group = Hq / Hkv;
+  sh.hc = heads_per_tile(group);
+  sh.chunks = group / sh.hc;
+  sh.tq = eca::kPfTile / sh.hc;
+  // At most so many units (pairs of query tiles per key/value head and chunk) of at most so many key tiles.
+  const double pairs = static_cast<double>(total_q) / (2 * sh.tq) + (total_q < B ? total_q : B);
+  const double tiles = (static_cast<double>(max_pages) * page_size + eca::kPfTile - 1) / eca::kPfTile;
+  const double most = pairs * Hkv * sh.chunks * (tiles + eca::kPfUnitCost) / eca::kPfMinCost + 1;
+  sh.grid = most < kPrefillMaxCtas ? static_cast<int>(most) : kPrefillMaxCtas;
+  sh.o_bytes = align256(2ull * sh.grid * 256 * D * 4);
+  sh.lse_bytes = align256(2ull * sh.grid * 256 * 4);
+  sh.bytes = sh.o_bytes + sh.lse_bytes + align256(4ull * sh.grid * eca::kPfSplitWords);
+  return sh;
+}
+
+template <int D, bool BF16, int FORM>
+int launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_cache, const eca::PrefillParams& p, int grid,
+                   const Device& dev, cudaStream_t stream) {
+  using L = eca::PrefillSmem<D>;
+  static std::atomic<uint64_t> done{0};
+  const int rc = configure(eca::paged_prefill_kernel<D, BF16, FORM>, dev, &done, L::kDynamicBytes,
+                           (256 * eca::kRegsSoftmax + 128 * eca::kRegsControl + eca::kPfThreads - 1) / eca::kPfThreads);
+  if (rc != ATTN_OK) return rc;
+  const int r = launched(launch_pdl(eca::paged_prefill_kernel<D, BF16, FORM>, static_cast<unsigned>(grid),
+                                    eca::kPfThreads, L::kDynamicBytes, stream, tm_q, tm_cache, p));
+  if (r != ATTN_OK) return r;
+  constexpr int kRows = 32;
+  return launched(launch_pdl(eca::paged_prefill_combine<D, BF16>, static_cast<unsigned>(grid * (256 / kRows)), 2 * D, 0,
+                             stream, p, kRows));
+}
+
 template <int D, bool BF16>
-int launch_prefill(const eca::PrefillParams& p, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.s.total) * p.Hq + 3) / 4);
-  return launched(launch_pdl(eca::paged_prefill_kernel<D, BF16>, grid, 128, 0, stream, p));
+int launch_prefill_form(const CUtensorMap& tm_q, const CUtensorMap& tm_cache, const eca::PrefillParams& p, int grid,
+                        const Device& dev, cudaStream_t stream) {
+  if (p.f.softcap > 0.f) return launch_prefill<D, BF16, eca::kFormCap>(tm_q, tm_cache, p, grid, dev, stream);
+  if (p.f.slopes != nullptr) return launch_prefill<D, BF16, eca::kFormBias>(tm_q, tm_cache, p, grid, dev, stream);
+  return launch_prefill<D, BF16, eca::kFormPlain>(tm_q, tm_cache, p, grid, dev, stream);
 }
 
 int prefill_impl(bool bf16, const void* q, const void* cache, const int* block_table, const int* lengths,
@@ -70,7 +143,7 @@ int prefill_impl(bool bf16, const void* q, const void* cache, const int* block_t
   int rc = check_paged_args(cache, block_table, lengths, B, Hkv, D, page_size, max_pages, num_pages);
   if (rc == ATTN_OK) rc = check_chunk_args(q, total_q, Hq, Hkv, D, scale, softcap, window, alibi_slopes, prefix_lens);
   if (rc != ATTN_OK) return rc;
-  if (!q_offsets || (!out && total_q > 0)) return ATTN_ERR_INVALID_ARG;
+  if (!q_offsets || (!out && total_q > 0) || B > eca::kPfMaxRequests) return ATTN_ERR_INVALID_ARG;
   if (!aligned(out, 16) || !aligned(q_offsets, 4) || (lse && !aligned(lse, 4))) return ATTN_ERR_UNALIGNED;
   if (total_q == 0) return ATTN_OK;
   const uint64_t qbytes = static_cast<uint64_t>(total_q) * Hq * D * 2;
@@ -78,26 +151,44 @@ int prefill_impl(bool bf16, const void* q, const void* cache, const int* block_t
       overlaps(out, qbytes, cache, cache_bytes(Hkv, D, page_size, num_pages))) {
     return ATTN_ERR_INVALID_ARG;
   }
-  const uint64_t need = attn_prefill_workspace_bytes(total_q, B, Hq, Hkv, D, page_size, max_pages);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
-    if (!aligned(workspace, 256)) return ATTN_ERR_UNALIGNED;
-    if (overlaps(workspace, need, q, qbytes) || overlaps(workspace, need, out, qbytes)) return ATTN_ERR_INVALID_ARG;
+  const PrefillShape sh = prefill_shape(total_q, B, Hq, Hkv, D, page_size, max_pages);
+  if (!workspace || workspace_bytes < sh.bytes) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return ATTN_ERR_UNALIGNED;
+  if (overlaps(workspace, sh.bytes, q, qbytes) || overlaps(workspace, sh.bytes, out, qbytes) ||
+      overlaps(workspace, sh.bytes, cache, cache_bytes(Hkv, D, page_size, num_pages))) {
+    return ATTN_ERR_INVALID_ARG;
   }
   Device dev;
   rc = current_device(&dev);
   if (rc != ATTN_OK) return rc;
   eca::PrefillParams p;
   p.s = chunk_shape(block_table, lengths, q_offsets, total_q, B, Hkv, D, page_size, max_pages, num_pages, dev.status);
-  p.f = eca::ScoreForm{scale, softcap, alibi_slopes, prefix_lens, window};
-  p.q = q;
-  p.cache = cache;
+  p.f = score_form(scale, softcap, window, alibi_slopes, prefix_lens, max_pages * page_size);
   p.out = out;
   p.lse = lse;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sh.o_bytes);
+  p.split = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + sh.o_bytes + sh.lse_bytes);
   p.Hq = Hq;
+  p.hc = sh.hc;
+  p.chunks = sh.chunks;
+  p.tq = sh.tq;
+  p.by_hc = eca::make_fast_div(sh.hc);
+  p.scale_log2e = scale * eca::kLog2e;
+  p.wait_limit_ns = kWaitLimitNs;
+  p.timeout_code = ATTN_ERR_TIMEOUT;
+  CUtensorMap tm_q, tm_cache;
+  rc = head_rows_map(&tm_q, q, bf16, D, Hq, total_q, static_cast<unsigned>(sh.hc), static_cast<unsigned>(sh.tq));
+  if (rc == ATTN_OK) rc = paged_cache_map(&tm_cache, cache, bf16, D, Hkv, page_size, num_pages);
+  if (rc != ATTN_OK) return rc;
+  const int grid = sh.grid < dev.sm_count ? sh.grid : dev.sm_count;  // one CTA per SM
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 128) return bf16 ? launch_prefill<128, true>(p, s) : launch_prefill<128, false>(p, s);
-  return bf16 ? launch_prefill<64, true>(p, s) : launch_prefill<64, false>(p, s);
+  if (D == 128) {
+    return bf16 ? launch_prefill_form<128, true>(tm_q, tm_cache, p, grid, dev, s)
+                : launch_prefill_form<128, false>(tm_q, tm_cache, p, grid, dev, s);
+  }
+  return bf16 ? launch_prefill_form<64, true>(tm_q, tm_cache, p, grid, dev, s)
+              : launch_prefill_form<64, false>(tm_q, tm_cache, p, grid, dev, s);
 }
 
 template <int D, bool BF16>
@@ -129,7 +220,7 @@ int mass_impl(bool bf16, const void* q, const float* lse, const void* cache, con
   if (rc != ATTN_OK) return rc;
   eca::MassParams p;
   p.s = chunk_shape(block_table, lengths, q_offsets, total_q, B, Hkv, D, page_size, max_pages, num_pages, dev.status);
-  p.f = eca::ScoreForm{scale, softcap, alibi_slopes, prefix_lens, window};
+  p.f = score_form(scale, softcap, window, alibi_slopes, prefix_lens, max_pages * page_size);
   p.q = q;
   p.cache = cache;
   p.lse = lse;
@@ -166,8 +257,9 @@ int attn_prefill_paged_bf16(const void* q, const void* cache, const int* block_t
 }
 
 size_t attn_prefill_workspace_bytes(int total_q, int B, int Hq, int Hkv, int D, int page_size, int max_pages) {
-  (void)total_q, (void)B, (void)Hq, (void)Hkv, (void)D, (void)page_size, (void)max_pages;
-  return 0;
+  if (total_q < 1 || B < 1 || B > eca::kPfMaxRequests || Hkv < 1 || Hq < 1 || Hq % Hkv != 0) return 0;
+  if ((D != 64 && D != 128) || max_pages < 1 || page_size < 8 || page_size > 64) return 0;
+  return static_cast<size_t>(prefill_shape(total_q, B, Hq, Hkv, D, page_size, max_pages).bytes);
 }
 
 int attn_paged_append_chunk(const void* new_kv, void* cache, const int* block_table, const int* lengths,

@@ -2,7 +2,6 @@
 // (request, key/value head, token), walking the chunk's rows and heads in order.
 #pragma once
 #include "paged_common.cuh"
-#include "paged_prefill.cuh"
 
 namespace eca {
 
@@ -16,6 +15,13 @@ struct MassParams {
   int accumulate;
   int Hq;
 };
+
+// Score of one key from q . k (natural units).
+__device__ __forceinline__ float form_score(const ScoreForm& f, float dot, float slope, int away) {
+  float x = dot * f.scale;
+  if (f.softcap > 0.f) x = f.softcap * tanhf(x / f.softcap);
+  return x - slope * fabsf(static_cast<float>(away));
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(128) paged_mass_kernel(const MassParams p) {

@@ -57,7 +57,7 @@ extern "C" {
  *   out         : device, [total_q, Hq, D] fp16; lse: device, [total_q, Hq] fp32 or
  *                 NULL.  Written for every row of a request; O = 0 and lse = -inf for a row that
  *                 sees no key.
- *   total_q     : >= 0 (0: nothing is launched).
+ *   total_q     : >= 0 (0: nothing is launched).   B : 1 .. 4096.
  *   workspace   : device, 256-byte aligned, at least attn_prefill_workspace_bytes of
  *                 the same sizes; its contents on entry do not matter.  Two calls must not share
  *                 one while both may be running (two captured graphs neither).
