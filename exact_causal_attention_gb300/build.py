@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 # The same sources with ECA_ANATOMY: the attention kernel records per-CTA milestone
 # stamps (a measurement aid; nothing else changes).
 ANATOMY_LIB_PATH = os.path.join(BUILD_DIR, "libeca_attn_anatomy.so")
-SOURCES = ["attn_api.cu", "cache_api.cu"]
+SOURCES = ["attn_api.cu", "cache_api.cu", "prefill_api.cu", "mass_api.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,84 +1,581 @@
-// Attention weight that every cached token received from a ragged chunk.  One warp per
-// (request, key/value head, token), walking the chunk's rows and heads in order.
+// Attention weight that every cached token received from a ragged chunk:
+//   mass[b, kvh, j] (+)= sum over rows r of b and heads h of kvh of e^(s(r, h, j) - lse[r, h]).
+//
+// The sum runs over the rows, so the product is taken the other way round: S^T = K Q^T with a tile of
+// 128 keys as the rows (a key is a TMEM lane, one thread sums its row without shuffles or atomics) and
+// a step of up to 128 (row, head) pairs as the columns.  K is read once, V not at all.
+// For one decode step a key tile meets one step of g columns and the kernel is bound by reading K;
+// for a chunk it is bound by the exponentials, one per (pair, key).
+//
+// A CTA takes an equal part of the line of key tiles (paged_plan.cuh), two tiles of one
+// (request, head) at a time, one per slot; their steps of queries stream through a ring that both share.
+// 384 threads: warps 0-3 and 4-7 sum slots 0 and 1, warp 8 produces key tiles from their pages, warp 9
+// issues the MMAs, warp 10 loads Q, warp 11 the columns' log-sum-exps (and slopes and positions).  S^T is
+// double-buffered per slot and read whole into registers, so the next product never waits for the sums.
+//
+// e^(s - lse) is taken as 2^(log2e (s - lse)) with the difference formed first in natural units: where
+// the weight matters s is near lse, so the one rounding of the difference is small.
 #pragma once
-#include "paged_common.cuh"
+#include <cuda.h>
+
+#include "attn_fwd_kernel.cuh"
+#include "paged_form.cuh"
+#include "paged_plan.cuh"
 
 namespace eca {
+
+constexpr int kMsThreads = 384;
+constexpr int kMsTile = 128;       // keys per tile
+constexpr int kMsCols = 128;       // most columns of a step
+constexpr int kMsTileCost = 2;     // a key tile's own cost, in steps
+constexpr int kMsQueue = 4;
+constexpr int kMsReaders = 11;
+constexpr int kMsColStages = 4;    // ring of the columns' values
+// Per key tile, which of its pages have a bad id.  The sums may trail the products by two steps
+// (four tiles), and the producer runs ahead of those by the ring.
+constexpr int kMsBadRing = 32;
 
 struct MassParams {
   ChunkShape s;
   ScoreForm f;
-  const void* q;      // [total, Hq, D] 16-bit
-  const void* cache;
   const float* lse;   // [total, Hq]
   float* mass;        // [B, Hkv, max_pages * page_size]
   int accumulate;
   int Hq;
+  int hc, chunks;     // query heads per step, and chunks of the group
+  int tq;             // tokens per step
+  uint32_t idesc;     // of the MMA: 128 x (hc tq rounded up to 16)
+  FastDiv by_hc;
+  unsigned long long wait_limit_ns;
+  int timeout_code;
 };
 
-// Score of one key from q . k (natural units).
-__device__ __forceinline__ float form_score(const ScoreForm& f, float dot, float slope, int away) {
-  float x = dot * f.scale;
-  if (f.softcap > 0.f) x = f.softcap * tanhf(x / f.softcap);
-  return x - slope * fabsf(static_cast<float>(away));
+template <int D>
+struct MassSmem {
+  static constexpr int kSub = D / 64;
+  static constexpr int kTileBytes = kSub * kSubTileBytes;
+  static constexpr int kKStages = D == 128 ? 4 : 6;
+  static constexpr int kQStages = D == 128 ? 2 : 4;
+  static constexpr int kKOff = 0;
+  static constexpr int kQOff = kKStages * kTileBytes;
+  static constexpr int kColOff = kQOff + kQStages * kTileBytes;  // fp32 [stages][3][128]: lse, slope, position
+  static constexpr int kColBytes = 3 * kMsCols * 4;
+  static constexpr int kBarOff = kColOff + kMsColStages * kColBytes;
+  static constexpr int kBarKFull = 0;
+  static constexpr int kBarKEmpty = kBarKFull + kKStages;
+  static constexpr int kBarQFull = kBarKEmpty + kKStages;
+  static constexpr int kBarQEmpty = kBarQFull + kQStages;
+  static constexpr int kBarColFull = kBarQEmpty + kQStages;
+  static constexpr int kBarColEmpty = kBarColFull + kMsColStages;
+  static constexpr int kBarS = kBarColEmpty + kMsColStages;  // + 2 slot + buffer
+  static constexpr int kBarSFree = kBarS + 4;                // + 2 slot + buffer
+  static constexpr int kBarUnitFull = kBarSFree + 4;
+  static constexpr int kBarUnitFree = kBarUnitFull + kMsQueue;
+  static constexpr int kBarDrain = kBarUnitFree + kMsQueue;
+  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr int kBadOff = kMiscOff + 8;
+  static constexpr int kQueueOff = (kBadOff + 4 * kMsBadRing + 15) & ~15;
+  static constexpr int kEntryInts = 16;
+  static constexpr int kScanOff = kQueueOff + kMsQueue * kEntryInts * 4;
+  static constexpr int kBytes = kScanOff + 16 * 8;
+  static constexpr int kDynamicBytes = kBytes + 1024;
+  static_assert(kLineTableBytes <= kColOff, "the plan's tables fit over the rings");
+  static_assert(kDynamicBytes <= 227 * 1024, "shared memory exceeds the per-block limit");
+};
+
+// Steps (query tiles of tq tokens) that see a key of tile kt: q0 .. q1 - 1.
+struct TileSteps {
+  int q0, q1;
+};
+__device__ __forceinline__ TileSteps tile_steps(const MassParams& p, int n, int pos0, int prefix, int len, int kt) {
+  const int kb = kt * kMsTile;
+  if (kb >= len || n == 0) return TileSteps{0, 0};
+  if (kb < prefix) return TileSteps{0, (n + p.tq - 1) / p.tq};
+  const int lo = max(0, kb - pos0);
+  const int hi = p.f.window > 0 ? static_cast<int>(min(static_cast<long long>(n),
+                                                       static_cast<long long>(kb) + kMsTile - 1 + p.f.window - pos0))
+                                : n;
+  if (lo >= hi) return TileSteps{0, 0};
+  return TileSteps{lo / p.tq, (hi + p.tq - 1) / p.tq};
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) paged_mass_kernel(const MassParams p) {
+// Two key tiles (or one) of one (request, head).
+struct MassUnit {
+  int steps;     // query tiles per chunk of heads; -1 past the last unit
+  int q0;        // first of them
+  int kt;        // key tile of slot 0; slot 1 has the next one
+  int two;       // slot 1 has one
+  int row0, n, pos0, len, prefix;
+  int kvh, b;
+};
+
+template <int D, bool BF16, int FORM>
+__global__ void __launch_bounds__(kMsThreads, 1)
+    paged_mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_cache,
+                      const MassParams p) {
+  using L = MassSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t sbase = (raw_base + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw_base);
+  auto bar = [&](int i) -> uint32_t { return sbase + L::kBarOff + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+  volatile uint32_t* bad_pages = reinterpret_cast<volatile uint32_t*>(smem + L::kBadOff);
+  volatile int* queue = reinterpret_cast<volatile int*>(smem + L::kQueueOff);
+  float* cols_s = reinterpret_cast<float*>(smem + L::kColOff);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
+  const int lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kKStages; ++s) {
+      mbar_init(bar(L::kBarKFull + s), 1);
+      mbar_init(bar(L::kBarKEmpty + s), 1);
+    }
+    for (int s = 0; s < L::kQStages; ++s) {
+      mbar_init(bar(L::kBarQFull + s), 1);
+      mbar_init(bar(L::kBarQEmpty + s), 1);
+    }
+    for (int s = 0; s < kMsColStages; ++s) {
+      mbar_init(bar(L::kBarColFull + s), 1);
+      mbar_init(bar(L::kBarColEmpty + s), 8);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(bar(L::kBarS + s), 1);
+      mbar_init(bar(L::kBarSFree + s), 4);
+    }
+    for (int q = 0; q < kMsQueue; ++q) {
+      mbar_init(bar(L::kBarUnitFull + q), 1);
+      mbar_init(bar(L::kBarUnitFree + q), kMsReaders);
+    }
+    mbar_init(bar(L::kBarDrain), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) tma_prefetch_map(&tm_cache);
+  if (warp == 10 && lane == 0) tma_prefetch_map(&tm_q);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
   grid_launch_dependents();
   grid_dependency_wait();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const Watchdog wd{abort_flag, p.s.status, p.wait_limit_ns, p.timeout_code};
+
+  // ------------------------------------------------------------------------ plan
+  const int B = p.s.B;
   const int most = p.s.max_pages * p.s.page_size;
-  const long long w = static_cast<long long>(blockIdx.x) * 4 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (w >= static_cast<long long>(p.s.B) * p.s.Hkv * most) return;
-  const int j = static_cast<int>(w % most);
-  const int kvh = static_cast<int>(w / most % p.s.Hkv), b = static_cast<int>(w / most / p.s.Hkv);
-  const Request r = load_request(p.s, &p.f, b);
-  float sum = 0.f;
-  if (j < r.len) {
-    const int log2T = 31 - __clz(p.s.page_size), group = p.Hq / p.s.Hkv;
-    bool seen = false;
-    int page = -1;
-    float2 kv[D / 64];
-    for (int i = 0; i < r.n; ++i) {
-      const int pos = r.pos0 + i;
-      if (!((j <= pos && (p.f.window == 0 || j > pos - p.f.window)) || j < r.prefix)) continue;
-      if (!seen) {
-        seen = true;
-        page = p.s.block_table[static_cast<size_t>(b) * p.s.max_pages + (j >> log2T)];
-        if (page < 0 || page >= p.s.num_pages) {
-          if (lane == 0) atomicExch(p.s.status, p.s.bad_index_code);
-          page = -1;
-        } else {
-          const size_t krow =
-              (static_cast<size_t>(page) * 2 * p.s.page_size + (j & (p.s.page_size - 1))) * p.s.Hkv + kvh;
-          const uint32_t* k = reinterpret_cast<const uint32_t*>(p.cache) + krow * (D / 2);
+  const LineTables line = line_tables(smem, reinterpret_cast<long long*>(smem + L::kScanOff));
+  // Written in full, a tile that no row sees is an item too.
+  auto items_of = [&](int n, int len) { return ((p.accumulate ? (n > 0 ? len : 0) : most) + kMsTile - 1) / kMsTile; };
+  auto items = [&](const int4& r) { return items_of(r.x, r.w); };
+  auto cost = [&](const int4& r, int i) {
+    const TileSteps t = tile_steps(p, r.x, r.y, r.z, r.w, i);
+    return t.q1 > t.q0 ? kMsTileCost + (t.q1 - t.q0) * p.chunks : 1;
+  };
+  const long long W = line_build<kMsThreads>(line, p.s, p.f, p.s.Hkv, items, cost);
+  const int cta = static_cast<int>(blockIdx.x), G = static_cast<int>(gridDim.x);
+  struct Place {
+    int b, head, tile;
+  };
+  // Whole tiles: a place past a tile's middle cuts behind it (its tile may then be one past the
+  // request's last, the same cut as the next head's tile 0).
+  auto locate = [&](long long x) -> Place {
+    const LinePlace at = line_locate(line, B, x, cost);
+    return Place{at.b, at.head, at.item + (2 * at.in >= at.cost ? 1 : 0)};
+  };
+  Place from = {B, 0, 0}, to = {B, 0, 0};
+  if (warp == 8 && W > 0) {
+    from = locate(cta * W / G);
+    if (cta + 1 < G) to = locate((cta + 1) * W / G);
+  }
+  fence_proxy_async_smem();  // the plan's reads and writes come before the rings' copies
+  __syncthreads();
+
+  int units_read = 0;
+  auto next_unit = [&](MassUnit& w, bool whole_warp) -> bool {
+    const int q = units_read % kMsQueue;
+    bool got = wd.wait(bar(L::kBarUnitFull + q), parity(units_read / kMsQueue));
+    if (whole_warp) got = __all_sync(0xffffffffu, got) != 0;
+    if (!got) return false;
+    volatile int* e = queue + q * L::kEntryInts;
+    int v[11];
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x) kv[x] = to_f32x2<BF16>(k[lane + 32 * x]);
+    for (int i = 0; i < 11; ++i) v[i] = e[i];
+    if (whole_warp) {
+#pragma unroll
+      for (int i = 0; i < 11; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+    }
+    w = MassUnit{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9], v[10]};
+    if (lane == 0) mbar_arrive(bar(L::kBarUnitFree + q));
+    ++units_read;
+    return true;
+  };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ key tiles, from pages
+    const int T = p.s.page_size;
+    const int log2T = 31 - __clz(T);
+    const int pages = kMsTile >> log2T;
+    // A key tile meets all its queries in one unit, so K is read once.
+    const uint64_t pol = policy_evict_first();
+    int it = 0, pushed = 0;
+    bool ok = true;
+    int b = from.b, head = from.head, tile = from.tile;
+    while (ok && b < B && b <= to.b) {
+      const Request r = load_request(p.s, &p.f, b);
+      const int n_items = items_of(r.n, r.len);
+      const int* table = p.s.block_table + static_cast<size_t>(b) * p.s.max_pages;
+      // The window reaches down to the first token's.
+      const int w0 = p.f.window > 0 ? max(0, r.pos0 - p.f.window + 1) : 0;
+      auto page_of = [&](int kt, bool* needed) -> int {
+        const int pg = kt * pages + lane;
+        const int tok = pg << log2T;
+        *needed = lane < pages && kt < n_items && tok < r.len && (tok < r.prefix || tok + T > w0);
+        return *needed ? table[pg] : 0;
+      };
+      for (; ok && head < p.s.Hkv && n_items > 0; ++head, tile = 0) {
+        const bool last = b == to.b && head == to.head;
+        const int stop = last ? min(to.tile, n_items) : n_items;
+        bool needed;
+        int id = page_of(tile, &needed);
+        while (ok && tile < stop) {
+          const TileSteps s0 = tile_steps(p, r.n, r.pos0, r.prefix, r.len, tile);
+          TileSteps s1 = {0, 0};
+          const bool seen = s0.q1 > s0.q0;
+          bool two = tile + 1 < stop;
+          if (two) {
+            s1 = tile_steps(p, r.n, r.pos0, r.prefix, r.len, tile + 1);
+            two = (s1.q1 > s1.q0) == seen;
+          }
+          const int q0 = two ? min(s0.q0, s1.q0) : s0.q0;
+          const int q1 = two ? max(s0.q1, s1.q1) : s0.q1;
+          const int q = pushed % kMsQueue;
+          if (!__all_sync(0xffffffffu, wd.wait(bar(L::kBarUnitFree + q), parity(pushed / kMsQueue) ^ 1u))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            volatile int* e = queue + q * L::kEntryInts;
+            e[0] = seen ? q1 - q0 : 0;
+            e[1] = q0;
+            e[2] = tile;
+            e[3] = two;
+            e[4] = r.row0;
+            e[5] = r.n;
+            e[6] = r.pos0;
+            e[7] = r.len;
+            e[8] = r.prefix;
+            e[9] = head;
+            e[10] = b;
+            mbar_arrive(bar(L::kBarUnitFull + q));
+          }
+          ++pushed;
+          for (int x = 0; x < (two ? 2 : 1); ++x) {
+            const bool good = needed && id >= 0 && id < p.s.num_pages;
+            const bool load = needed;
+            const int my_id = id;
+            id = page_of(tile + x + 1, &needed);  // the next tile's ids are on their way while this one loads
+            if (!seen) continue;
+            const uint32_t bad = __ballot_sync(0xffffffffu, load && !good);
+            if (load && !good) atomicExch(p.s.status, p.s.bad_index_code);
+            const int slot = it % L::kKStages;
+            if (!__all_sync(0xffffffffu, wd.wait(bar(L::kBarKEmpty + slot), parity(it / L::kKStages) ^ 1u))) {
+              ok = false;
+              break;
+            }
+            const uint32_t full = bar(L::kBarKFull + slot);
+            if (lane == 0) {
+              bad_pages[it % kMsBadRing] = bad;
+              mbar_arrive_expect_tx(full, L::kTileBytes);
+            }
+            __syncwarp();
+            if (lane < pages) {
+              const uint32_t dst = sbase + L::kKOff + slot * L::kTileBytes + (lane << log2T) * 128;
+              const int z = good ? my_id * 2 * T : p.s.num_pages * 2 * T;  // out of range: zeros
+#pragma unroll
+              for (int s = 0; s < L::kSub; ++s) {
+                tma_load_3d(dst + s * kSubTileBytes, &tm_cache, full, 64 * s, head, z, pol);
+              }
+            }
+            ++it;
+          }
+          tile += two ? 2 : 1;
+        }
+        if (last) {
+          b = B;  // done
+          break;
         }
       }
-      if (page < 0) break;
-      for (int h = kvh * group; h < (kvh + 1) * group; ++h) {
-        const size_t row = static_cast<size_t>(r.row0 + i) * p.Hq + h;
-        const float lse = p.lse[row];
-        if (lse == -INFINITY) continue;
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q) + row * (D / 2);
-        float dot = 0.f;
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          const float2 qv = to_f32x2<BF16>(q[lane + 32 * x]);
-          dot += qv.x * kv[x].x + qv.y * kv[x].y;
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-        sum += expf(form_score(p.f, dot, p.f.slopes != nullptr ? p.f.slopes[h] : 0.f, pos - j) - lse);
+      ++b;
+      head = tile = 0;
+    }
+    if (ok) {
+      const int q = pushed % kMsQueue;
+      if (__all_sync(0xffffffffu, wd.wait(bar(L::kBarUnitFree + q), parity(pushed / kMsQueue) ^ 1u)) && lane == 0) {
+        queue[q * L::kEntryInts] = -1;
+        mbar_arrive(bar(L::kBarUnitFull + q));
       }
     }
-    if (p.accumulate && !seen) return;
-  } else if (p.accumulate) {
-    return;
+    for (int x = (it > L::kKStages ? it - L::kKStages : 0); x < it; ++x) {
+      wd.drain(bar(L::kBarKFull + x % L::kKStages), parity(x / L::kKStages));
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ MMA issuer
+    const uint64_t k_desc = smem_desc_sw128(sbase + L::kKOff, 16, 1024);
+    const uint64_t q_desc = smem_desc_sw128(sbase + L::kQOff, 16, 1024);
+    auto warp_wait = [&](uint32_t b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, wd.wait(b, ph)) != 0; };
+    int it = 0, step = 0;
+    int uses[2] = {0, 0};  // steps of each slot so far
+    bool ok = true;
+    MassUnit w;
+    while (ok) {
+      if (!next_unit(w, true) || w.steps < 0) break;
+      if (w.steps == 0) continue;
+      const int tiles = 1 + w.two;
+      for (int x = 0; ok && x < tiles; ++x) {
+        const int item = it + x;
+        ok = warp_wait(bar(L::kBarKFull + item % L::kKStages), parity(item / L::kKStages));
+      }
+      if (!ok) break;
+      const int n = w.steps * p.chunks;
+      for (int i = 0; i < n; ++i, ++step) {
+        const int qs = step % L::kQStages;
+        if (!warp_wait(bar(L::kBarQFull + qs), parity(step / L::kQStages))) {
+          ok = false;
+          break;
+        }
+        for (int x = 0; x < tiles; ++x) {
+          const int buf = uses[x] & 1;
+          if (!warp_wait(bar(L::kBarSFree + 2 * x + buf), parity(uses[x] / 2) ^ 1u)) {
+            ok = false;
+            break;
+          }
+          ++uses[x];
+          tc_fence_after_sync();
+          const uint64_t a = k_desc + static_cast<uint64_t>(((it + x) % L::kKStages) * (L::kTileBytes >> 4));
+          const uint64_t bq = q_desc + static_cast<uint64_t>(qs * (L::kTileBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>((kk / 4) * (kSubTileBytes >> 4) + (kk % 4) * 2);
+            mma_ss_warp(tmem + 256u * x + 128u * buf, a + off, bq + off, p.idesc, kk > 0 ? 1u : 0u);
+          }
+          tc_commit_warp(bar(L::kBarS + 2 * x + buf));
+        }
+        if (!ok) break;
+        tc_commit_warp(bar(L::kBarQEmpty + qs));
+      }
+      for (int x = 0; ok && x < tiles; ++x) tc_commit_warp(bar(L::kBarKEmpty + (it + x) % L::kKStages));
+      it += tiles;
+    }
+    tc_commit_warp(bar(L::kBarDrain));
+    wd.drain(bar(L::kBarDrain), 0);
+  } else if (warp == 10) {
+    // --------------------------------------------------------------------- Q loader
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last();  // every key tile of the request meets these rows
+      const uint32_t bytes = static_cast<uint32_t>(L::kSub * p.hc * p.tq * 128);
+      int step = 0;
+      bool ok = true;
+      MassUnit w;
+      while (ok && next_unit(w, false) && w.steps >= 0) {
+        for (int i = 0; i < w.steps * p.chunks; ++i, ++step) {
+          const int qs = step % L::kQStages;
+          if (!wd.wait(bar(L::kBarQEmpty + qs), parity(step / L::kQStages) ^ 1u)) {
+            ok = false;
+            break;
+          }
+          const int chunk = i / w.steps, qt = w.q0 + i % w.steps;
+          mbar_arrive_expect_tx(bar(L::kBarQFull + qs), bytes);
+          for (int s = 0; s < L::kSub; ++s) {
+            tma_load_3d(sbase + L::kQOff + qs * L::kTileBytes + s * kSubTileBytes, &tm_q, bar(L::kBarQFull + qs), 64 * s,
+                        (w.kvh * p.chunks + chunk) * p.hc, w.row0 + qt * p.tq, pol);
+          }
+        }
+      }
+      for (int x = (step > L::kQStages ? step - L::kQStages : 0); x < step; ++x) {
+        wd.drain(bar(L::kBarQFull + x % L::kQStages), parity(x / L::kQStages));
+      }
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------- the columns' values, lane by column
+    int tok[4], head[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      tok[i] = fast_div(lane + 32 * i, p.by_hc);
+      head[i] = lane + 32 * i - tok[i] * p.hc;
+    }
+    int step = 0;
+    bool ok = true;
+    MassUnit w;
+    while (ok && next_unit(w, true) && w.steps >= 0) {
+      const int n = w.steps * p.chunks;
+      float next[4];
+      // Infinity (no weight) for a column of no row and for a row that saw no key.
+      auto load = [&](int i) {
+        const int chunk = i / w.steps, t0 = (w.q0 + i % w.steps) * p.tq;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          next[c] = INFINITY;
+          if (tok[c] < p.tq && t0 + tok[c] < w.n) {
+            const float z = p.lse[static_cast<size_t>(w.row0 + t0 + tok[c]) * p.Hq + (w.kvh * p.chunks + chunk) * p.hc + head[c]];
+            next[c] = z == -INFINITY ? INFINITY : z;
+          }
+        }
+      };
+      if (n > 0) load(0);
+      for (int i = 0; i < n; ++i, ++step) {
+        const int cs = step % kMsColStages;
+        float now[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) now[c] = next[c];
+        const int chunk = i / w.steps, t0 = (w.q0 + i % w.steps) * p.tq;
+        if (i + 1 < n) load(i + 1);
+        if (!__all_sync(0xffffffffu, wd.wait(bar(L::kBarColEmpty + cs), parity(step / kMsColStages) ^ 1u))) {
+          ok = false;
+          break;
+        }
+        float* dst = cols_s + cs * 3 * kMsCols;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          dst[lane + 32 * c] = now[c];
+          if (FORM != kFormPlain && p.f.slopes != nullptr) {
+            dst[kMsCols + lane + 32 * c] = p.f.slopes[(w.kvh * p.chunks + chunk) * p.hc + head[c]];
+            dst[2 * kMsCols + lane + 32 * c] = static_cast<float>(w.pos0 + t0 + tok[c]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarColFull + cs));
+      }
+    }
+  } else {
+    // -------------------------------------------------------------------------- sums
+    const int x = warp / 4;  // slot
+    const int r_local = (warp % 4) * 32 + lane;
+    const uint32_t t_s = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + 256u * x;
+    const int log2T = 31 - __clz(p.s.page_size);
+    auto warp_wait = [&](uint32_t b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, wd.wait(b, ph)) != 0; };
+    const CapScale cap = cap_scale(p.f.scale, p.f.softcap, 1.f);
+    int it = 0, step = 0, uses = 0;
+    bool ok = true;
+    MassUnit w;
+    while (ok) {
+      if (!next_unit(w, true) || w.steps < 0) break;
+      const int n = w.steps * p.chunks;
+      const int item = it + x;
+      if (n > 0) it += 1 + w.two;
+      if (x > w.two) {
+        // No tile for this slot: it still hands the steps' columns back.
+        for (int i = 0; i < n; ++i, ++step) {
+          const int cs = step % kMsColStages;
+          if (!warp_wait(bar(L::kBarColFull + cs), parity(step / kMsColStages))) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kBarColEmpty + cs));
+        }
+        continue;
+      }
+      const int key = (w.kt + x) * kMsTile + r_local;
+      const float key_f = static_cast<float>(key);
+      // Tokens that see this key: from .. upto - 1 of the request.
+      int from_tok = max(0, key - w.pos0), upto = w.n;
+      if (key < w.prefix) {
+        from_tok = 0;
+      } else if (key >= w.len) {
+        upto = 0;
+      } else if (p.f.window > 0) {
+        upto = static_cast<int>(min(static_cast<long long>(w.n), static_cast<long long>(key) + p.f.window - w.pos0));
+      }
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t bad = 0;
+      for (int i = 0; i < n; ++i, ++step) {
+        const int t0 = (w.q0 + i % w.steps) * p.tq;
+        const int cols = min(p.tq, w.n - t0) * p.hc;
+        // Columns of this step that see this key.
+        const int lo = (max(from_tok, t0) - t0) * p.hc, hi = min(cols, (min(upto, t0 + p.tq) - t0) * p.hc);
+        const int buf = uses & 1;
+        if (!warp_wait(bar(L::kBarS + 2 * x + buf), parity(uses / 2))) {
+          ok = false;
+          break;
+        }
+        ++uses;
+        tc_fence_after_sync();
+        if (i == 0) bad = bad_pages[item % kMsBadRing];
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (32 * q < cols) tmem_ld_x32(t_s + 128u * buf + 32u * q, s[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_wait_ld_x32(s[q]);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarSFree + 2 * x + buf));
+        const int cs = step % kMsColStages;
+        if (!warp_wait(bar(L::kBarColFull + cs), parity(step / kMsColStages))) {
+          ok = false;
+          break;
+        }
+        const float* col = cols_s + cs * 3 * kMsCols;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (32 * q < cols) {
+            if constexpr (FORM == kFormCap) cap_scores(s[q], cap);
+            const float c = FORM == kFormCap ? 1.f : p.f.scale;
+            const bool all = __all_sync(0xffffffffu, lo <= 32 * q && hi >= 32 * q + 32);
+#pragma unroll
+            for (int i4 = 0; i4 < 32; i4 += 4) {
+              const float4 z = *reinterpret_cast<const float4*>(col + 32 * q + i4);
+              float y[4] = {fmaf(__uint_as_float(s[q][i4]), c, -z.x), fmaf(__uint_as_float(s[q][i4 + 1]), c, -z.y),
+                            fmaf(__uint_as_float(s[q][i4 + 2]), c, -z.z), fmaf(__uint_as_float(s[q][i4 + 3]), c, -z.w)};
+              if (FORM != kFormPlain && p.f.slopes != nullptr) {
+                const float4 sl = *reinterpret_cast<const float4*>(col + kMsCols + 32 * q + i4);
+                const float4 ps = *reinterpret_cast<const float4*>(col + 2 * kMsCols + 32 * q + i4);
+                y[0] = fmaf(-sl.x, fabsf(ps.x - key_f), y[0]);
+                y[1] = fmaf(-sl.y, fabsf(ps.y - key_f), y[1]);
+                y[2] = fmaf(-sl.z, fabsf(ps.z - key_f), y[2]);
+                y[3] = fmaf(-sl.w, fabsf(ps.w - key_f), y[3]);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float v = ex2(y[e] * kLog2e);
+                const int at = 32 * q + i4 + e;
+                if (all) {
+                  acc[e] += v;
+                } else if (at >= lo && at < hi) {
+                  acc[e] += v;
+                }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarColEmpty + cs));
+      }
+      if (!ok) break;
+      if (key < most && (n > 0 || !p.accumulate)) {
+        const bool skipped = ((bad >> (r_local >> log2T)) & 1u) != 0;
+        const float sum = skipped ? 0.f : (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        float* dst = p.mass + (static_cast<size_t>(w.b) * p.s.Hkv + w.kvh) * most + key;
+        *dst = p.accumulate ? *dst + sum : sum;
+      }
+    }
   }
-  if (lane == 0) p.mass[w] = p.accumulate ? p.mass[w] + sum : sum;
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 }  // namespace eca

@@ -1,0 +1,164 @@
+// Sharing out work whose sizes live on the device.  Every request has items (pairs of query
+// tiles, key tiles) that cost something, each once per head.  Laid end to end
+// (request, head, item) they form a line; every CTA lays it out for itself and takes its
+// equal part, so that nothing is counted or waited for across CTAs and the parts
+// are the same whenever the sizes are.
+#pragma once
+#include "paged_common.cuh"
+
+namespace eca {
+
+constexpr int kPlanMaxRequests = 4096;
+
+// Shared-memory tables of the line, free again once the CTA knows its part.
+struct LineTables {
+  int4* req;                 // [B]: n, pos0, prefix, len
+  unsigned long long* cost;  // [B]: of one head
+  long long* base;           // [B + 1]: where the request starts on the line
+  int* first;                // [B + 1]: items of the requests before
+  long long* warp_sums;      // [warps]
+};
+constexpr int kLineTableBytes = 16 * kPlanMaxRequests + 8 * kPlanMaxRequests + 8 * (kPlanMaxRequests + 2) +
+                                4 * (kPlanMaxRequests + 4);
+
+__device__ __forceinline__ LineTables line_tables(uint8_t* smem, long long* warp_sums) {
+  LineTables t;
+  t.req = reinterpret_cast<int4*>(smem);
+  t.cost = reinterpret_cast<unsigned long long*>(smem + 16 * kPlanMaxRequests);
+  t.base = reinterpret_cast<long long*>(smem + 24 * kPlanMaxRequests);
+  t.first = reinterpret_cast<int*>(smem + 32 * kPlanMaxRequests + 16);
+  t.warp_sums = warp_sums;
+  return t;
+}
+
+// The last i in [0, n) with a[i] <= x, for a[0] <= x and a in order.
+template <typename T, typename X>
+__device__ __forceinline__ int last_at_most(const T* a, int n, X x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a[mid] <= x) {
+      lo = mid;
+    } else {
+      hi = mid;
+    }
+  }
+  return lo;
+}
+
+// Inclusive sum over the block in thread order.
+template <int kThreads>
+__device__ __forceinline__ long long line_scan(long long v, long long* warp_sums, long long* total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long up = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += up;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const long long x = warp_sums[w];
+    if (w < warp) before += x;
+    all += x;
+  }
+  *total = all;
+  return before + v;
+}
+
+// Lays the line out; called by the whole block.  items(req) and cost(req, item) of a
+// request's int4.  Returns the line's length.
+template <int kThreads, typename Items, typename Cost>
+__device__ __forceinline__ long long line_build(const LineTables& t, const ChunkShape& s, const ScoreForm& f, int heads,
+                                                Items items, Cost cost) {
+  const int B = s.B, tid = threadIdx.x;
+  int count = 0;
+  for (int b0 = 0; b0 < B; b0 += kThreads) {
+    const int b = b0 + tid;
+    int mine = 0;
+    if (b < B) {
+      const Request r = load_request(s, &f, b);
+      t.req[b] = make_int4(r.n, r.pos0, r.prefix, r.len);
+      t.cost[b] = 0;
+      mine = items(t.req[b]);
+    }
+    long long all;
+    const long long upto = line_scan<kThreads>(mine, t.warp_sums, &all);
+    if (b < B) t.first[b] = count + static_cast<int>(upto) - mine;
+    count += static_cast<int>(all);
+  }
+  if (tid == 0) t.first[B] = count;
+  __syncthreads();
+  for (int i = tid; i < count; i += kThreads) {
+    const int b = last_at_most(t.first, B, i);
+    atomicAdd(t.cost + b, static_cast<unsigned long long>(cost(t.req[b], i - t.first[b])));
+  }
+  __syncthreads();
+  long long length = 0;
+  for (int b0 = 0; b0 < B; b0 += kThreads) {
+    const int b = b0 + tid;
+    const long long mine = b < B ? static_cast<long long>(t.cost[b]) * heads : 0;
+    long long all;
+    const long long upto = line_scan<kThreads>(mine, t.warp_sums, &all);
+    if (b < B) t.base[b] = length + upto - mine;
+    length += all;
+  }
+  if (tid == 0) t.base[B] = length;
+  __syncthreads();
+  return length;
+}
+
+// The item that holds place x of the line.
+struct LinePlace {
+  int b, head, item;
+  int in;           // x, from the item's start
+  int cost;         // the item's
+  long long start;  // of the item, on the line
+};
+
+// Called by a whole warp; x below the line's length.
+template <typename Cost>
+__device__ __forceinline__ LinePlace line_locate(const LineTables& t, int B, long long x, Cost cost) {
+  const int lane = threadIdx.x % 32;
+  LinePlace r;
+  // Requests without items share their base with the next: the last such one has items.
+  r.b = last_at_most(t.base, B, x);
+  const long long sum = static_cast<long long>(t.cost[r.b]);
+  const long long in = x - t.base[r.b];
+  r.head = static_cast<int>(in / sum);
+  long long rest = in - r.head * sum;
+  r.start = x - rest;
+  const int4 q = t.req[r.b];
+  const int n = t.first[r.b + 1] - t.first[r.b];
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    const int mine = i < n ? cost(q, i) : 0;
+    long long c = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long up = __shfl_up_sync(0xffffffffu, c, d);
+      if (lane >= d) c += up;
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, i < n && rest < c);
+    if (here != 0) {
+      const int src = __ffs(here) - 1;
+      const long long before = __shfl_sync(0xffffffffu, c - mine, src);
+      r.item = i0 + src;
+      r.cost = __shfl_sync(0xffffffffu, mine, src);
+      r.in = static_cast<int>(rest - before);
+      r.start += before;
+      return r;
+    }
+    const long long all = __shfl_sync(0xffffffffu, c, 31);
+    rest -= all;
+    r.start += all;
+  }
+  r.item = n;  // not reached: a request's items cover its stretch
+  r.cost = r.in = 0;
+  return r;
+}
+
+}  // namespace eca

@@ -33,13 +33,13 @@
 #include <cuda.h>
 
 #include "attn_fwd_kernel.cuh"
-#include "paged_common.cuh"
+#include "paged_form.cuh"
+#include "paged_plan.cuh"
 
 namespace eca {
 
 constexpr int kPfThreads = 384;
 constexpr int kPfTile = 128;          // keys per tile, and rows per query tile
-constexpr int kPfMaxRequests = 4096;  // the plan's tables lie over the K/V ring
 // What starting and ending a unit costs, in key tiles, and the least work a part of
 // the line is cut to.
 constexpr int kPfUnitCost = 3;
@@ -51,11 +51,6 @@ constexpr int kPfReaders = 11;
 // before it hands P_j over, so before V_j's place in the ring is free: the producer is
 // then at most 10 places (5 tiles) further.
 constexpr int kPfBadRing = 8;
-
-// Score forms as the kernel's template argument.
-constexpr int kFormPlain = 0;
-constexpr int kFormBias = 1;  // distance bias
-constexpr int kFormCap = 2;   // tanh cap, with or without a bias
 
 struct PrefillParams {
   ChunkShape s;
@@ -105,13 +100,8 @@ struct PrefillSmem {
   static constexpr int kScanOff = kQueueOff + kPfQueue * kEntryInts * 4;  // 12 warps' sums, 64-bit
   static constexpr int kBytes = kScanOff + 16 * 8;
   static constexpr int kDynamicBytes = kBytes + 1024;
-  // The plan's tables, over the ring: per request its sizes, its first unit row and its first place
-  // on the line of costs.
-  static constexpr int kPlanReqOff = kRingOff;                               // int4 [B]
-  static constexpr int kPlanSumOff = kPlanReqOff + 16 * kPfMaxRequests;      // int64 [B]: cost of one head
-  static constexpr int kPlanBaseOff = kPlanSumOff + 8 * kPfMaxRequests;      // int64 [B + 1]
-  static constexpr int kPlanPairOff = kPlanBaseOff + 8 * (kPfMaxRequests + 2);  // int32 [B + 1]
-  static_assert(kPlanPairOff + 4 * (kPfMaxRequests + 1) <= kBarOff, "the plan's tables fit over the ring");
+  // The plan's tables lie over the ring.
+  static_assert(kLineTableBytes <= kStages * kTileBytes, "the plan's tables fit over the ring");
   static_assert(kDynamicBytes <= 227 * 1024, "shared memory exceeds the per-block limit");
 };
 
@@ -152,14 +142,6 @@ __device__ __forceinline__ int cut_tile(long long y, int k) {
   return static_cast<int>(t);
 }
 
-// tanh(y) = 1 - 2 / (1 + e^2y), for any y.
-__device__ __forceinline__ float tanh_wide(float y) {
-  const float e = ex2(y * (2.f * kLog2e));
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
-  return fmaf(-2.f, r, 1.f);
-}
-
 // A fragment of a unit as the producer hands it to the other warps.
 struct Fragment {
   int n_max;        // key tiles; -1 past the last fragment
@@ -188,11 +170,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   volatile uint32_t* bad_pages = reinterpret_cast<volatile uint32_t*>(smem + L::kBadOff);
   volatile int* queue = reinterpret_cast<volatile int*>(smem + L::kQueueOff);
   long long* scan_s = reinterpret_cast<long long*>(smem + L::kScanOff);
-  int4* plan_req = reinterpret_cast<int4*>(smem + L::kPlanReqOff);
-  unsigned long long* plan_sum = reinterpret_cast<unsigned long long*>(smem + L::kPlanSumOff);
-  long long* plan_base = reinterpret_cast<long long*>(smem + L::kPlanBaseOff);
-  int* plan_pair = reinterpret_cast<int*>(smem + L::kPlanPairOff);
-
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
   const int lane = threadIdx.x % 32;
   const int tid = threadIdx.x;
@@ -239,127 +216,24 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int B = p.s.B;
   const int heads = p.s.Hkv * p.chunks;  // units of a pair
   const int per_pair = 2 * p.tq;
-  // Inclusive scan over the block, in thread order.
-  auto scan = [&](long long v, long long* total) -> long long {
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const long long up = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v += up;
-    }
-    __syncthreads();
-    if (lane == 31) scan_s[warp] = v;
-    __syncthreads();
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kPfThreads / 32; ++w) {
-      const long long x = scan_s[w];
-      if (w < warp) before += x;
-      all += x;
-    }
-    *total = all;
-    return before + v;
-  };
-  int pairs = 0;
-  for (int b0 = 0; b0 < B; b0 += kPfThreads) {
-    const int b = b0 + tid;
-    int mine = 0;
-    if (b < B) {
-      const Request r = load_request(p.s, &p.f, b);
-      mine = (r.n + per_pair - 1) / per_pair;
-      plan_req[b] = make_int4(r.n, r.pos0, r.prefix, r.len);
-      plan_sum[b] = 0;
-    }
-    long long all;
-    const long long upto = scan(mine, &all);
-    if (b < B) plan_pair[b] = pairs + static_cast<int>(upto) - mine;
-    pairs += static_cast<int>(all);
-  }
-  if (tid == 0) plan_pair[B] = pairs;
-  __syncthreads();
-  for (int i = tid; i < pairs; i += kPfThreads) {
-    int lo = 0, hi = B;  // plan_pair[lo] <= i < plan_pair[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (plan_pair[mid] <= i) {
-        lo = mid;
-      } else {
-        hi = mid;
-      }
-    }
-    const int4 r = plan_req[lo];
-    const int k = pair_tiles(p, r.x, r.y, r.z, i - plan_pair[lo]).k;
-    atomicAdd(plan_sum + lo, static_cast<unsigned long long>(k + kPfUnitCost));
-  }
-  __syncthreads();
-  long long W = 0;
-  for (int b0 = 0; b0 < B; b0 += kPfThreads) {
-    const int b = b0 + tid;
-    const long long mine = b < B ? static_cast<long long>(plan_sum[b]) * heads : 0;
-    long long all;
-    const long long upto = scan(mine, &all);
-    if (b < B) plan_base[b] = W + upto - mine;
-    W += all;
-  }
-  if (tid == 0) plan_base[B] = W;
-  __syncthreads();
+  const LineTables line = line_tables(smem + L::kRingOff, scan_s);
+  auto items = [&](const int4& r) { return (r.x + per_pair - 1) / per_pair; };
+  auto cost = [&](const int4& r, int i) { return pair_tiles(p, r.x, r.y, r.z, i).k + kPfUnitCost; };
+  const long long W = line_build<kPfThreads>(line, p.s, p.f, heads, items, cost);
   const int grid = static_cast<int>(gridDim.x);
   const int cta = static_cast<int>(blockIdx.x);
   const long long most = W / kPfMinCost;
   const int G = most < 1 ? 1 : (most < grid ? static_cast<int>(most) : grid);
 
-  // A place on the line: the unit that holds it, and where it cuts it.
+  // A place on the line: the unit that holds it, and the key tile before which it cuts it.
   struct Place {
     int b, head, pair, tile, k;
     long long start;  // of the unit, on the line
   };
-  // Called by a whole warp; x < W.
   auto locate = [&](long long x) -> Place {
-    Place r;
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (plan_base[mid] <= x) {
-        lo = mid;
-      } else {
-        hi = mid;
-      }
-    }
-    // Requests without rows share their base with the next: the last such lo has units.
-    r.b = lo;
-    const long long sum = static_cast<long long>(plan_sum[lo]);
-    const long long in = x - plan_base[lo];
-    r.head = static_cast<int>(in / sum);
-    long long rest = in - r.head * sum;
-    r.start = x - rest;
-    const int4 q = plan_req[lo];
-    const int np = plan_pair[lo + 1] - plan_pair[lo];
-    for (int p0 = 0; p0 < np; p0 += 32) {
-      const int pr = p0 + lane;
-      const int k = pr < np ? pair_tiles(p, q.x, q.y, q.z, pr).k : 0;
-      long long c = pr < np ? k + kPfUnitCost : 0;
-      const long long mine = c;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const long long up = __shfl_up_sync(0xffffffffu, c, d);
-        if (lane >= d) c += up;
-      }
-      const unsigned here = __ballot_sync(0xffffffffu, pr < np && rest < c);
-      const long long all = __shfl_sync(0xffffffffu, c, 31);
-      if (here != 0) {
-        const int src = __ffs(here) - 1;
-        r.pair = p0 + src;
-        r.k = __shfl_sync(0xffffffffu, k, src);
-        const long long before = __shfl_sync(0xffffffffu, c - mine, src);
-        r.tile = cut_tile(rest - before, r.k);
-        r.start += before;
-        return r;
-      }
-      rest -= all;
-      r.start += all;
-    }
-    r.pair = np;  // not reached: the request's pairs cover its line
-    r.k = r.tile = 0;
-    return r;
+    const LinePlace at = line_locate(line, B, x, cost);
+    const int k = at.cost - kPfUnitCost;
+    return Place{at.b, at.head, at.item, cut_tile(at.in, k), k, at.start};
   };
   Place from = {}, to = {};
   const bool has_work = cta < G && W > 0;
@@ -688,8 +562,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const uint32_t t_o = tmem + lane_base + 256u + static_cast<uint32_t>(D) * t;
     // Scores arrive as q . k; the form turns them into the base-2 domain.
     const float c = FORM == kFormPlain ? p.scale_log2e : 1.f;
-    const float cap2 = FORM == kFormCap ? p.f.softcap * kLog2e : 0.f;
-    const float cap_in = FORM == kFormCap ? p.f.scale / p.f.softcap : 0.f;
+    const CapScale cap = cap_scale(p.f.scale, p.f.softcap, kLog2e);
     const int row_tok = fast_div(r_local, p.by_hc);  // this row's token and head within the tile
     const int row_head = r_local - row_tok * p.hc;
     const int T = p.s.page_size;
@@ -737,10 +610,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         auto form_quarter = [&](int q) {
           if constexpr (FORM == kFormPlain) return;
           if constexpr (FORM == kFormCap) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              s[q][i] = __float_as_uint(cap2 * tanh_wide(__uint_as_float(s[q][i]) * cap_in));
-            }
+            cap_scores(s[q], cap);
             if (p.f.slopes == nullptr) return;
           }
           const float away = static_cast<float>(pos - kb - 32 * q);
