@@ -44,6 +44,7 @@ struct MassParams {
   int Hq;
   int hc, chunks;     // query heads per step, and chunks of the group
   int tq;             // tokens per step
+  int small_plan;     // the line is laid out by one warp
   uint32_t idesc;     // of the MMA: 128 x (hc tq rounded up to 16)
   FastDiv by_hc;
   unsigned long long wait_limit_ns;
@@ -178,7 +179,13 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     const TileSteps t = tile_steps(p, r.x, r.y, r.z, r.w, i);
     return t.q1 > t.q0 ? kMsTileCost + (t.q1 - t.q0) * p.chunks : 1;
   };
-  const long long W = line_build<kMsThreads>(line, p.s, p.f, p.s.Hkv, items, cost);
+  // Only the producer needs the plan; a long one is laid out by the whole block.
+  long long W = 0;
+  if (!p.small_plan) {
+    W = line_build<kMsThreads>(line, p.s, p.f, p.s.Hkv, items, cost);
+  } else if (warp == 8) {
+    W = line_build_warp(line, p.s, p.f, p.s.Hkv, items, cost);
+  }
   const int cta = static_cast<int>(blockIdx.x), G = static_cast<int>(gridDim.x);
   struct Place {
     int b, head, tile;
@@ -191,10 +198,11 @@ __global__ void __launch_bounds__(kMsThreads, 1)
   };
   Place from = {B, 0, 0}, to = {B, 0, 0};
   if (warp == 8 && W > 0) {
-    from = locate(cta * W / G);
-    if (cta + 1 < G) to = locate((cta + 1) * W / G);
+    from = locate(line_cut(W, G, cta));
+    if (cta + 1 < G) to = locate(line_cut(W, G, cta + 1));
   }
-  fence_proxy_async_smem();  // the plan's reads and writes come before the rings' copies
+  // The plan's reads and writes come before the rings' copies and the columns' values.
+  fence_proxy_async_smem();
   __syncthreads();
 
   int units_read = 0;

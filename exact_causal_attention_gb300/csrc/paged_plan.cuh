@@ -111,6 +111,68 @@ __device__ __forceinline__ long long line_build(const LineTables& t, const Chunk
   return length;
 }
 
+// The same by one warp, without the block's barriers, for at most 32 requests and few
+// enough items that 32 lanes get through them as fast (line_is_small).
+template <typename Items, typename Cost>
+__device__ __forceinline__ long long line_build_warp(const LineTables& t, const ChunkShape& s, const ScoreForm& f,
+                                                     int heads, Items items, Cost cost) {
+  const int B = s.B, b = threadIdx.x % 32;
+  int4 req = make_int4(0, 0, 0, 0);
+  int mine = 0;
+  if (b < B) {
+    const Request r = load_request(s, &f, b);
+    req = make_int4(r.n, r.pos0, r.prefix, r.len);
+    mine = items(req);
+  }
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int up = __shfl_up_sync(0xffffffffu, upto, d);
+    if (b >= d) upto += up;
+  }
+  long long sum = 0;
+  for (int r = 0; r < B; ++r) {
+    const int4 q = make_int4(__shfl_sync(0xffffffffu, req.x, r), __shfl_sync(0xffffffffu, req.y, r),
+                             __shfl_sync(0xffffffffu, req.z, r), __shfl_sync(0xffffffffu, req.w, r));
+    const int n = __shfl_sync(0xffffffffu, mine, r);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      // A cost is below 2^25 (key tiles of a context below 2^31 tokens), so 32 of them fit.
+      const int c = __reduce_add_sync(0xffffffffu, i0 + b < n ? cost(q, i0 + b) : 0);
+      if (b == r) sum += c;
+    }
+  }
+  long long end = sum * heads;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long up = __shfl_up_sync(0xffffffffu, end, d);
+    if (b >= d) end += up;
+  }
+  if (b < B) {
+    t.req[b] = req;
+    t.cost[b] = static_cast<unsigned long long>(sum);
+    t.base[b] = end - sum * heads;
+    t.first[b] = upto - mine;
+    if (b == B - 1) {
+      t.base[B] = end;
+      t.first[B] = upto;
+    }
+  }
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, end, B - 1);
+}
+
+// Is a line of B requests and at most `total` items short enough for line_build_warp?
+__host__ inline bool line_is_small(int B, double total) { return B <= 32 && total / 32 + B <= 64; }
+
+// Where the c-th of G equal parts of a line of length W starts.
+__device__ __forceinline__ long long line_cut(long long W, int G, int c) {
+  if (W < (1ll << 32)) {  // 32-bit divisions take a fraction of the time
+    const uint32_t w = static_cast<uint32_t>(W), g = static_cast<uint32_t>(G);
+    return static_cast<long long>(w / g) * c + (w % g) * static_cast<uint32_t>(c) / g;
+  }
+  return W / G * c + W % G * c / G;
+}
+
 // The item that holds place x of the line.
 struct LinePlace {
   int b, head, item;
@@ -128,7 +190,8 @@ __device__ __forceinline__ LinePlace line_locate(const LineTables& t, int B, lon
   r.b = last_at_most(t.base, B, x);
   const long long sum = static_cast<long long>(t.cost[r.b]);
   const long long in = x - t.base[r.b];
-  r.head = static_cast<int>(in / sum);
+  r.head = ((in | sum) >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(sum))
+                                   : static_cast<int>(in / sum);
   long long rest = in - r.head * sum;
   r.start = x - rest;
   const int4 q = t.req[r.b];

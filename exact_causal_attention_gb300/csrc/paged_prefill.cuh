@@ -43,7 +43,7 @@ constexpr int kPfTile = 128;          // keys per tile, and rows per query tile
 // What starting and ending a unit costs, in key tiles, and the least work a part of
 // the line is cut to.
 constexpr int kPfUnitCost = 3;
-constexpr int kPfMinCost = 5;
+constexpr int kPfMinCost = 4;
 constexpr int kPfMinPart = 2;         // a unit is not cut within so many tiles of its ends
 constexpr int kPfQueue = 4;
 constexpr int kPfReaders = 11;
@@ -65,6 +65,7 @@ struct PrefillParams {
   int chunks;         // of the group: Hq / Hkv / hc
   int tq;             // tokens per query tile
   FastDiv by_hc;
+  int small_plan;     // the line is laid out by one warp
   float scale_log2e;
   unsigned long long wait_limit_ns;
   int timeout_code;
@@ -151,7 +152,7 @@ struct Fragment {
   int head;         // first query head
   int pos;          // position of the first token
   int prefix, len;
-  int pre, gap, kv; // logical tile of the fragment's j-th: v = kv + j, v < pre ? v : v + gap
+  int pre, gap, kv; // its tiles are kv .. kv + n_max - 1, taken from the last down; v < pre ? v : v + gap
   int part;         // partial slot, or -1: the whole unit
 };
 
@@ -219,9 +220,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const LineTables line = line_tables(smem + L::kRingOff, scan_s);
   auto items = [&](const int4& r) { return (r.x + per_pair - 1) / per_pair; };
   auto cost = [&](const int4& r, int i) { return pair_tiles(p, r.x, r.y, r.z, i).k + kPfUnitCost; };
-  const long long W = line_build<kPfThreads>(line, p.s, p.f, heads, items, cost);
   const int grid = static_cast<int>(gridDim.x);
   const int cta = static_cast<int>(blockIdx.x);
+  // Only the producer needs the plan; a long one is laid out by the whole block.
+  long long W = 0;
+  if (!p.small_plan) {
+    W = line_build<kPfThreads>(line, p.s, p.f, heads, items, cost);
+  } else if (warp == 8) {
+    W = line_build_warp(line, p.s, p.f, heads, items, cost);
+  }
   const long long most = W / kPfMinCost;
   const int G = most < 1 ? 1 : (most < grid ? static_cast<int>(most) : grid);
 
@@ -238,15 +245,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   Place from = {}, to = {};
   const bool has_work = cta < G && W > 0;
   if (warp == 8 && has_work) {
-    from = locate(cta * W / G);
+    from = locate(line_cut(W, G, cta));
     if (cta + 1 < G) {
-      to = locate((cta + 1) * W / G);
+      to = locate(line_cut(W, G, cta + 1));
     } else {
       to.b = B;
     }
   }
-  fence_proxy_async_smem();  // the plan's reads and writes come before the ring's copies
-  __syncthreads();
+  // The plan's reads and writes come before the ring's copies (which this warp issues).
+  fence_proxy_async_smem();
+  if (!p.small_plan) {
+    __syncthreads();
+  } else {
+    __syncwarp();
+  }
   // The unit that starts here and ends in a later CTA: for the combine kernel.
   if (warp == 8 && lane == 0) {
     int parts = 0;
@@ -256,7 +268,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (!started_before) {
         parts = 2;
         for (int c = cta + 2; c < G; ++c) {
-          const long long y = c * W / G - to.start;
+          const long long y = line_cut(W, G, c) - to.start;
           if (y >= to.k + kPfUnitCost || cut_tile(y, to.k) >= to.k) break;
           ++parts;
         }
@@ -371,7 +383,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           // K/V that several units read stays in L2; a lone pair's is read once.
           const uint64_t pol = r.n > per_pair ? policy_evict_last() : policy_evict_first();
           auto page_of = [&](int j, bool* needed) -> int {
-            const int v = tile + j;
+            const int v = tile + w.n_max - 1 - j;
             const int pg = (v < u.pre ? v : v + u.gap) * pages + lane;
             const int tok = pg << log2T;
             *needed = lane < pages && j < w.n_max && (tok < r.prefix || (tok + T > u.w0 && tok < u.hi));
@@ -480,15 +492,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (!next_fragment(w, true) || w.n_max < 0) break;
         if (w.n_max == 0) continue;
         const int n_kv = t ? w.n1 : w.n0;
+        const int first = w.n_max - n_kv;  // tiles that this query tile does not look at
         // Items of the fragment: K_j at it + 2 j, V_j behind it.  Every item is waited for and released
         // by both issuers.
         if ((n_kv > 0 && !warp_wait(bar(L::kBarQFull + t), parity(used))) || !item_wait(it)) break;
         tc_fence_after_sync();
         if (!take_turn()) break;
-        if (n_kv > 0) issue_qk<D, BF16>(s_tmem, q_desc, k_desc + stage_off(it));
+        if (first == 0) issue_qk<D, BF16>(s_tmem, q_desc, k_desc + stage_off(it));
         pass_turn();
-        if (n_kv > 0) tc_commit_warp(bar(L::kBarS + t));
-        if (n_kv == 1) tc_commit_warp(bar(L::kBarQFree + t));
+        if (first == 0) {
+          tc_commit_warp(bar(L::kBarS + t));
+          if (w.n_max == 1) tc_commit_warp(bar(L::kBarQFree + t));
+        }
         tc_commit_warp(bar(L::kBarEmpty + it % L::kStages));
         for (int j = 0; j < w.n_max; ++j) {
           const int xv = it + 2 * j + 1, xk = xv + 1;
@@ -496,9 +511,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             ok = false;
             break;
           }
-          if (j < n_kv) {
+          if (j >= first) {
             // O_t is overwritten by a unit's first P V: the epilogue before must have read it.
-            if (j == 0 && used > 0 && !warp_wait(bar(L::kBarOFree + t), parity(used - 1))) {
+            if (j == first && used > 0 && !warp_wait(bar(L::kBarOFree + t), parity(used - 1))) {
               ok = false;
               break;
             }
@@ -513,8 +528,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             ok = false;
             break;
           }
-          if (j < n_kv) {
-            issue_pv<D, BF16>(o_tmem, s_tmem, v_desc + stage_off(xv), j > 0, 0, 4);
+          if (j >= first) {
+            issue_pv<D, BF16>(o_tmem, s_tmem, v_desc + stage_off(xv), j > first, 0, 4);
             if (!warp_wait(bar(L::kBarPb + t), parity(p_waits - 1))) {
               ok = false;
               break;
@@ -527,19 +542,19 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               ok = false;
               break;
             }
-            if (j + 1 < n_kv) {
+            if (j + 1 >= first) {
               tc_fence_after_sync();
               issue_qk<D, BF16>(s_tmem, q_desc, k_desc + stage_off(xk));
             }
           }
           pass_turn();
-          if (j < n_kv) {
-            if (j + 1 < n_kv) {
+          if (j + 1 < w.n_max) {
+            if (j + 1 >= first) {
               tc_commit_warp(bar(L::kBarS + t));
-              if (j + 2 == n_kv) tc_commit_warp(bar(L::kBarQFree + t));
-            } else {
-              tc_commit_warp(bar(L::kBarO + t));
+              if (j + 2 == w.n_max) tc_commit_warp(bar(L::kBarQFree + t));
             }
+          } else if (n_kv > 0) {
+            tc_commit_warp(bar(L::kBarO + t));
           }
           tc_commit_warp(bar(L::kBarEmpty + xv % L::kStages));
           if (j + 1 < w.n_max) tc_commit_warp(bar(L::kBarEmpty + xk % L::kStages));
@@ -589,8 +604,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (FORM != kFormPlain && p.f.slopes != nullptr && row_ok) slope2 = p.f.slopes[w.head + row_head] * kLog2e;
       float m_ref = -INFINITY;
       float l = 0.f;
-      for (int j = 0; j < n_kv; ++j) {
-        const int v = w.kv + j;
+      const int first = w.n_max - n_kv;
+      for (int j = first; j < w.n_max; ++j) {
+        const int v = w.kv + w.n_max - 1 - j;
         const int kb = (v < w.pre ? v : v + w.gap) * kPfTile;  // position of the tile's first key
         // Columns this row sees: [0, pe) and [ws, ce).
         const int pe = w.prefix - kb, ce = pos + 1 - kb;
@@ -605,148 +621,34 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const bool tail = w.len - kb < kPfTile && (w.len & (T - 1)) != 0;  // the context ends inside one of its pages
         const bool full = pe >= kPfTile || (ws <= 0 && ce >= kPfTile) || !row_ok;
         const bool masked = __any_sync(0xffffffffu, !full) || bad != 0 || tail;
-        uint32_t s[4][32];
-        // Base-2 scores of quarter q from q . k.
-        auto form_quarter = [&](int q) {
-          if constexpr (FORM == kFormPlain) return;
-          if constexpr (FORM == kFormCap) {
-            cap_scores(s[q], cap);
-            if (p.f.slopes == nullptr) return;
+        // Rows of V behind the context's last token, on its last page, may hold anything: zeros,
+        // before P is handed over.
+        auto zero_tail = [&]() -> bool {
+          const int x = it0 + 2 * j + 1;
+          if (!warp_wait(bar(L::kBarFull + x % L::kStages), parity(x / L::kStages))) return false;
+          const int z0 = max(0, w.len - kb), z1 = min(kPfTile, (((w.len + T - 1) >> log2T) << log2T) - kb);
+          const uint32_t base = sbase + L::kRingOff + (x % L::kStages) * L::kTileBytes;
+          for (int i = r_local; i < (z1 - z0) * L::kSub * 8; i += 128) {
+            const int row = z0 + i / (L::kSub * 8), at = i % (L::kSub * 8);
+            st_shared_v4(base + (at / 8) * kSubTileBytes + row * 128 + (at % 8) * 16, 0u, 0u, 0u, 0u);
           }
-          const float away = static_cast<float>(pos - kb - 32 * q);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float x = FORM == kFormBias ? __uint_as_float(s[q][i]) * p.scale_log2e : __uint_as_float(s[q][i]);
-            s[q][i] = __float_as_uint(fmaf(-slope2, fabsf(away - static_cast<float>(i)), x));
-          }
+          fence_proxy_async_smem();
+          return true;
         };
-        auto load_scores = [&]() {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld_x32(t_s + 32u * q, s[q]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_wait_ld_x32(s[q]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) form_quarter(q);
-          if (masked) {
-            auto low = [](int n) -> uint32_t { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); };
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t seen = low(pe - 32 * q) | (low(ce - 32 * q) & ~low(ws - 32 * q));
-              if (bad != 0) {
-                for (int i = 0; i < 32; ++i) {
-                  if ((bad >> ((32 * q + i) >> log2T)) & 1u) seen &= ~(1u << i);
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if (!(seen & (1u << i))) s[q][i] = __float_as_uint(-INFINITY);
-              }
+        // Columns of quarter q that this row sees, as bits.
+        auto seen_bits = [&](int q) -> uint32_t {
+          auto low = [](int n) -> uint32_t { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); };
+          uint32_t seen = low(pe - 32 * q) | (low(ce - 32 * q) & ~low(ws - 32 * q));
+          if (bad != 0) {
+#pragma unroll 1
+            for (int i = 0; i < 32; i += 8) {  // a page holds 8 tokens at least
+              if ((bad >> ((32 * q + i) >> log2T)) & 1u) seen &= ~(0xffu << i);
             }
           }
+          return seen;
         };
-        uint32_t pk[2][32];
-        auto exp_quarters = [&](int q0, int q1, float neg_m, float2 (&acc)[8]) {
-          const float2 c2 = make_float2(c, c);
-          const float2 nm2 = make_float2(neg_m, neg_m);
-#pragma unroll
-          for (int q = q0; q < q1; ++q) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), c2, nm2);
-              const float2 e = make_float2(ex2(x.x), ex2(x.y));
-              acc[(i / 2) % 8] = __fadd2_rn(acc[(i / 2) % 8], e);
-              pk[q / 2][(q % 2) * 16 + i / 2] = pack2<BF16>(e.x, e.y);
-            }
-          }
-        };
-        auto row_total = [](const float2 (&acc)[8]) -> float {
-          const float2 a = __fadd2_rn(__fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3])),
-                                      __fadd2_rn(__fadd2_rn(acc[4], acc[5]), __fadd2_rn(acc[6], acc[7])));
-          return a.x + a.y;
-        };
-        auto exponentiate = [&](float neg_m) -> float {
-          float2 acc[8];
-#pragma unroll
-          for (int a = 0; a < 8; ++a) acc[a] = make_float2(0.f, 0.f);
-          exp_quarters(0, 4, neg_m, acc);
-          return row_total(acc);
-        };
-        float alpha = 1.f;
-        float row_sum = 0.f;
-        bool move = true;  // the first key tile takes the row max
-        if (j > 0) {
-          if (masked) {
-            load_scores();
-            row_sum = exponentiate(-m_ref);
-            move = !(row_sum <= max_row_sum<BF16>());  // (also an inf or NaN sum)
-          } else {
-            // Keys 64-127 load while keys 0-63 are exponentiated; the checks that let
-            // a stale reference stand are those of the dense kernel.
-            tmem_ld_x32(t_s, s[0]);
-            tmem_ld_x32(t_s + 32u, s[1]);
-            tmem_wait_ld_x32(s[0]);
-            tmem_wait_ld_x32(s[1]);
-            tmem_ld_x32(t_s + 64u, s[2]);
-            tmem_ld_x32(t_s + 96u, s[3]);
-            form_quarter(0);
-            form_quarter(1);
-            float2 acc[8];
-#pragma unroll
-            for (int a = 0; a < 8; ++a) acc[a] = make_float2(0.f, 0.f);
-            exp_quarters(0, 2, -m_ref, acc);
-            const float sum_a = row_total(acc);
-            tmem_wait_ld_x32(s[2]);
-            tmem_wait_ld_x32(s[3]);
-            form_quarter(2);
-            form_quarter(3);
-            float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              mx[0] = fmax3(mx[0], __uint_as_float(s[2][i]), __uint_as_float(s[2][i + 1]));
-              mx[1] = fmax3(mx[1], __uint_as_float(s[3][i]), __uint_as_float(s[3][i + 1]));
-            }
-            const float top_b = fmaxf(mx[0], mx[1]) * c - m_ref;
-            const bool fast = !row_ok || (sum_a <= max_row_sum<BF16>() && top_b <= max_lead<BF16>());
-            if (__all_sync(0xffffffffu, fast)) {
-              tmem_st_x32(t_s, pk[0]);
-              tmem_wait_st();
-              tc_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(L::kBarPa + t));
-#pragma unroll
-              for (int a = 0; a < 8; ++a) acc[a] = make_float2(0.f, 0.f);
-              exp_quarters(2, 4, -m_ref, acc);
-              tmem_st_x32(t_s + 32u, pk[1]);
-              tmem_wait_st();
-              tc_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(L::kBarPb + t));
-              l += sum_a + row_total(acc);
-              continue;
-            }
-            move = !fast;
-          }
-        }
-        if (__any_sync(0xffffffffu, move && row_ok) || j == 0) {
-          load_scores();  // S is still intact in TMEM: P has not been stored yet
-          if (move) {
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) mx[q] = fmax3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
-            }
-            const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            const float m_new = j == 0 ? m_tile : fmaxf(m_ref, m_tile);
-            alpha = (j == 0 || m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
-            m_ref = m_new;
-          }
-          row_sum = exponentiate(m_ref == -INFINITY ? 0.f : -m_ref);
-        }
-        l = l * alpha + row_sum;
-        tmem_st_x32(t_s, pk[0]);
-        tmem_st_x32(t_s + 32u, pk[1]);
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // O rescaled in TMEM (P V of the tile before is complete: S was committed after it).
+        auto rescale_o = [&](float alpha) {
           const float2 al2 = make_float2(alpha, alpha);
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 32) {
@@ -761,29 +663,148 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             tmem_st_x32(t_o + c0, o);
           }
+        };
+        auto row_total = [](const float2 (&acc)[8]) -> float {
+          const float2 a = __fadd2_rn(__fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3])),
+                                      __fadd2_rn(__fadd2_rn(acc[4], acc[5]), __fadd2_rn(acc[6], acc[7])));
+          return a.x + a.y;
+        };
+        // P's half h is in its place in TMEM: hand it to the issuer.
+        auto hand_over = [&](int b) {
+          tmem_wait_st();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(b + t));
+        };
+        bool move = j == first;  // take the row's max as the reference
+        if (FORM == kFormPlain && j > first && !masked) {
+          // One pass against the reference as it stands.  Keys 64-127 load while keys 0-63 are
+          // exponentiated; the checks that let a stale reference stand are those of the dense kernel.
+          uint32_t s[4][32];
+          uint32_t pk[2][32];
+          auto exp_quarters = [&](int q0, int q1) -> float {
+            float2 acc[8];
+#pragma unroll
+            for (int a = 0; a < 8; ++a) acc[a] = make_float2(0.f, 0.f);
+            const float2 c2 = make_float2(c, c);
+            const float2 nm2 = make_float2(-m_ref, -m_ref);
+#pragma unroll
+            for (int q = q0; q < q1; ++q) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), c2, nm2);
+                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                acc[(i / 2) % 8] = __fadd2_rn(acc[(i / 2) % 8], e);
+                pk[q / 2][(q % 2) * 16 + i / 2] = pack2<BF16>(e.x, e.y);
+              }
+            }
+            return row_total(acc);
+          };
+          tmem_ld_x32(t_s, s[0]);
+          tmem_ld_x32(t_s + 32u, s[1]);
+          tmem_wait_ld_x32(s[0]);
+          tmem_wait_ld_x32(s[1]);
+          tmem_ld_x32(t_s + 64u, s[2]);
+          tmem_ld_x32(t_s + 96u, s[3]);
+          const float sum_a = exp_quarters(0, 2);
+          tmem_wait_ld_x32(s[2]);
+          tmem_wait_ld_x32(s[3]);
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            mx[0] = fmax3(mx[0], __uint_as_float(s[2][i]), __uint_as_float(s[2][i + 1]));
+            mx[1] = fmax3(mx[1], __uint_as_float(s[3][i]), __uint_as_float(s[3][i + 1]));
+          }
+          const float top_b = fmaxf(mx[0], mx[1]) * c - m_ref;
+          const bool fast = !row_ok || (sum_a <= max_row_sum<BF16>() && top_b <= max_lead<BF16>());
+          if (__all_sync(0xffffffffu, fast)) {
+            tmem_st_x32(t_s, pk[0]);
+            hand_over(L::kBarPa);
+            const float sum_b = exp_quarters(2, 4);
+            tmem_st_x32(t_s + 32u, pk[1]);
+            hand_over(L::kBarPb);
+            l += sum_a + sum_b;
+            continue;
+          }
+          move = !fast;  // S is still intact in TMEM: P has not been stored yet
         }
-        // Rows of V behind the context's last token, on its last page, may hold anything: zeros.
-        if (tail) {
-          const int x = it0 + 2 * j + 1;
-          if (!warp_wait(bar(L::kBarFull + x % L::kStages), parity(x / L::kStages))) {
-            ok = false;
-            break;
+        // Two passes: the first applies the form and the mask, takes the row's max and writes the scores
+        // back, the second exponentiates them against a reference that is known to hold.  (The first
+        // is a loop: with the form's code inlined four times and more the softmax warps waited for
+        // instructions.)
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32];
+          tmem_ld_x32(t_s + 32u * q, s);
+          tmem_wait_ld_x32(s);
+          if constexpr (FORM == kFormCap) cap_scores(s, cap);
+          if (FORM == kFormBias || (FORM == kFormCap && p.f.slopes != nullptr)) {
+            const float away = static_cast<float>(pos - kb - 32 * q);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float x = FORM == kFormBias ? __uint_as_float(s[i]) * p.scale_log2e : __uint_as_float(s[i]);
+              s[i] = __float_as_uint(fmaf(-slope2, fabsf(away - static_cast<float>(i)), x));
+            }
           }
-          const int z0 = max(0, w.len - kb), z1 = min(kPfTile, (((w.len + T - 1) >> log2T) << log2T) - kb);
-          const uint32_t base = sbase + L::kRingOff + (x % L::kStages) * L::kTileBytes;
-          for (int i = r_local; i < (z1 - z0) * L::kSub * 8; i += 128) {
-            const int row = z0 + i / (L::kSub * 8), at = i % (L::kSub * 8);
-            st_shared_v4(base + (at / 8) * kSubTileBytes + row * 128 + (at % 8) * 16, 0u, 0u, 0u, 0u);
+          if (masked) {
+            const uint32_t seen = seen_bits(q);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (!(seen & (1u << i))) s[i] = __float_as_uint(-INFINITY);
+            }
           }
-          fence_proxy_async_smem();
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) top = fmax3(top, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          if (FORM != kFormPlain || masked) tmem_st_x32(t_s + 32u * q, s);
+        }
+        top *= c;
+        // The reference moves on the first tile, and when a p could leave the 16-bit range.
+        float alpha = 1.f;
+        if (move || top > m_ref + max_lead<BF16>()) {
+          const float m_new = j == first ? top : fmaxf(m_ref, top);
+          alpha = (j == first || m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
+          m_ref = m_new;
+        }
+        l *= alpha;
+        if (j > first && __any_sync(0xffffffffu, alpha != 1.f)) rescale_o(alpha);
+        if (tail && !zero_tail()) {
+          ok = false;
+          break;
         }
         tmem_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(L::kBarPa + t));
-          mbar_arrive(bar(L::kBarPb + t));
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        const float2 c2 = make_float2(c, c);
+        const float2 nm2 = make_float2(neg_m, neg_m);
+        float2 acc[8];
+#pragma unroll
+        for (int a = 0; a < 8; ++a) acc[a] = make_float2(0.f, 0.f);
+        uint32_t s[2][32];
+        tmem_ld_x32(t_s, s[0]);
+        tmem_ld_x32(t_s + 32u, s[1]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          tmem_wait_ld_x32(s[0]);
+          tmem_tie_x32(s[1]);
+          uint32_t pk[32];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), c2, nm2);
+              const float2 e = make_float2(ex2(x.x), ex2(x.y));
+              acc[(i / 2) % 8] = __fadd2_rn(acc[(i / 2) % 8], e);
+              pk[q * 16 + i / 2] = pack2<BF16>(e.x, e.y);
+            }
+          }
+          tmem_st_x32(t_s + 32u * half, pk);
+          if (half == 0) {
+            tmem_ld_x32(t_s + 64u, s[0]);
+            tmem_ld_x32(t_s + 96u, s[1]);
+          }
+          hand_over(half == 0 ? L::kBarPa : L::kBarPb);
         }
+        l += row_total(acc);
       }
       if (!ok) break;
       if (n_kv > 0) {
@@ -814,7 +835,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         p.part_lse[static_cast<size_t>(w.part) * 256 + t * 128 + r_local] = row_ok ? lse2 : -INFINITY;
       } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * D);
+        // 32 columns at a time.  Four lanes exchange 16-byte chunks, so that each then writes a
+        // quarter of 64 bytes of one row: a store touches 8 rows instead of 32 (which took 4 times as long).
+        const int q0 = lane & ~3, qj = lane & 3;
+        uint16_t* dst[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = wq * 32 + q0 + i;
+          const int rt = fast_div(r, p.by_hc);
+          dst[i] = rt < toks ? static_cast<uint16_t*>(p.out) +
+                                   (static_cast<size_t>(w.row + t * p.tq + rt) * p.Hq + w.head + r - rt * p.hc) * D + 8 * qj
+                             : nullptr;
+        }
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t o[32];
@@ -822,17 +854,34 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             tmem_ld_x32(t_o + c0, o);
             tmem_wait_ld_x32(o);
           }
-          if (row_ok) {
+          uint32_t h[4][4];  // [chunk][word]
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 h = make_uint4(0u, 0u, 0u, 0u);
-              if (any) {
-                h.x = pack2<BF16>(__uint_as_float(o[8 * i]) * inv_l, __uint_as_float(o[8 * i + 1]) * inv_l);
-                h.y = pack2<BF16>(__uint_as_float(o[8 * i + 2]) * inv_l, __uint_as_float(o[8 * i + 3]) * inv_l);
-                h.z = pack2<BF16>(__uint_as_float(o[8 * i + 4]) * inv_l, __uint_as_float(o[8 * i + 5]) * inv_l);
-                h.w = pack2<BF16>(__uint_as_float(o[8 * i + 6]) * inv_l, __uint_as_float(o[8 * i + 7]) * inv_l);
+          for (int i = 0; i < 16; ++i) {
+            h[i / 4][i % 4] = any ? pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l) : 0u;
+          }
+          // Transpose of 4 lanes x 4 chunks: first between neighbours, then between pairs.
+#pragma unroll
+          for (int d = 1; d < 4; d *= 2) {
+            const bool upper = (qj & d) != 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              if (x & d) continue;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t give = upper ? h[x][k] : h[x | d][k];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, d);
+                if (upper) {
+                  h[x][k] = got;
+                } else {
+                  h[x | d][k] = got;
+                }
               }
-              dst[c0 / 8 + i] = h;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (dst[i] != nullptr) {
+              *reinterpret_cast<uint4*>(dst[i] + c0) = make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]);
             }
           }
         }

@@ -94,6 +94,7 @@ int prefill_impl(bool bf16, const void* q, const void* cache, const int* block_t
   p.chunks = sh.chunks;
   p.tq = sh.tq;
   p.by_hc = eca::make_fast_div(sh.hc);
+  p.small_plan = eca::line_is_small(B, static_cast<double>(total_q) / (2 * sh.tq) + B);
   p.scale_log2e = scale * eca::kLog2e;
   p.wait_limit_ns = kWaitLimitNs;
   p.timeout_code = ATTN_ERR_TIMEOUT;
