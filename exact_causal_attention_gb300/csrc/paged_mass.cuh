@@ -59,7 +59,7 @@ struct MassSmem {
   static constexpr int kQStages = D == 128 ? 2 : 4;
   static constexpr int kKOff = 0;
   static constexpr int kQOff = kKStages * kTileBytes;
-  static constexpr int kColOff = kQOff + kQStages * kTileBytes;  // fp32 [stages][3][128]: lse, slope, position
+  static constexpr int kColOff = kQOff + kQStages * kTileBytes;  // fp32 [stages][3][128]: - lse, slope, position
   static constexpr int kColBytes = 3 * kMsCols * 4;
   static constexpr int kBarOff = kColOff + kMsColStages * kColBytes;
   static constexpr int kBarKFull = 0;
@@ -424,15 +424,15 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     while (ok && next_unit(w, true) && w.steps >= 0) {
       const int n = w.steps * p.chunks;
       float next[4];
-      // Infinity (no weight) for a column of no row and for a row that saw no key.
+      // Minus the log-sum-exp; minus infinity (no weight) for a column of no row and for a row that saw no key.
       auto load = [&](int i) {
         const int chunk = i / w.steps, t0 = (w.q0 + i % w.steps) * p.tq;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          next[c] = INFINITY;
+          next[c] = -INFINITY;
           if (tok[c] < p.tq && t0 + tok[c] < w.n) {
             const float z = p.lse[static_cast<size_t>(w.row0 + t0 + tok[c]) * p.Hq + (w.kvh * p.chunks + chunk) * p.hc + head[c]];
-            next[c] = z == -INFINITY ? INFINITY : z;
+            next[c] = z == -INFINITY ? z : -z;
           }
         }
       };
@@ -501,67 +501,98 @@ __global__ void __launch_bounds__(kMsThreads, 1)
       } else if (p.f.window > 0) {
         upto = static_cast<int>(min(static_cast<long long>(w.n), static_cast<long long>(key) + p.f.window - w.pos0));
       }
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 acc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
       uint32_t bad = 0;
       for (int i = 0; i < n; ++i, ++step) {
-        const int t0 = (w.q0 + i % w.steps) * p.tq;
+        const int t0 = (w.q0 + (p.chunks == 1 ? i : i % w.steps)) * p.tq;
         const int cols = min(p.tq, w.n - t0) * p.hc;
         // Columns of this step that see this key.
         const int lo = (max(from_tok, t0) - t0) * p.hc, hi = min(cols, (min(upto, t0 + p.tq) - t0) * p.hc);
         const int buf = uses & 1;
+        const uint32_t t_b = t_s + 128u * buf;
         if (!warp_wait(bar(L::kBarS + 2 * x + buf), parity(uses / 2))) {
           ok = false;
           break;
         }
         ++uses;
         tc_fence_after_sync();
+        uint32_t s[2][32];
+        tmem_ld_x32(t_b, s[0]);
         if (i == 0) bad = bad_pages[item % kMsBadRing];
-        uint32_t s[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (32 * q < cols) tmem_ld_x32(t_s + 128u * buf + 32u * q, s[q]);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_wait_ld_x32(s[q]);
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kBarSFree + 2 * x + buf));
         const int cs = step % kMsColStages;
         if (!warp_wait(bar(L::kBarColFull + cs), parity(step / kMsColStages))) {
           ok = false;
           break;
         }
         const float* col = cols_s + cs * 3 * kMsCols;
+        const int quarters = (cols + 31) / 32;
+        // Sums 32 columns: 2^(log2e (form(s) - lse)).
+        auto add = [&](uint32_t (&v)[32], int q) {
+          if constexpr (FORM == kFormCap) cap_scores(v, cap);
+          const float2 c2 = make_float2(p.f.scale, p.f.scale), k2 = make_float2(kLog2e, kLog2e);
+          const bool biased = FORM == kFormBias || (FORM == kFormCap && p.f.slopes != nullptr);
+          const bool all = __all_sync(0xffffffffu, lo <= 32 * q && hi >= 32 * q + 32) != 0;
+          auto low = [](int m) -> uint32_t { return m <= 0 ? 0u : (m >= 32 ? ~0u : (1u << m) - 1u); };
+          const uint32_t seen = low(hi - 32 * q) & ~low(lo - 32 * q);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (32 * q < cols) {
-            if constexpr (FORM == kFormCap) cap_scores(s[q], cap);
-            const float c = FORM == kFormCap ? 1.f : p.f.scale;
-            const bool all = __all_sync(0xffffffffu, lo <= 32 * q && hi >= 32 * q + 32);
-#pragma unroll
-            for (int i4 = 0; i4 < 32; i4 += 4) {
-              const float4 z = *reinterpret_cast<const float4*>(col + 32 * q + i4);
-              float y[4] = {fmaf(__uint_as_float(s[q][i4]), c, -z.x), fmaf(__uint_as_float(s[q][i4 + 1]), c, -z.y),
-                            fmaf(__uint_as_float(s[q][i4 + 2]), c, -z.z), fmaf(__uint_as_float(s[q][i4 + 3]), c, -z.w)};
-              if (FORM != kFormPlain && p.f.slopes != nullptr) {
-                const float4 sl = *reinterpret_cast<const float4*>(col + kMsCols + 32 * q + i4);
-                const float4 ps = *reinterpret_cast<const float4*>(col + 2 * kMsCols + 32 * q + i4);
-                y[0] = fmaf(-sl.x, fabsf(ps.x - key_f), y[0]);
-                y[1] = fmaf(-sl.y, fabsf(ps.y - key_f), y[1]);
-                y[2] = fmaf(-sl.z, fabsf(ps.z - key_f), y[2]);
-                y[3] = fmaf(-sl.w, fabsf(ps.w - key_f), y[3]);
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float v = ex2(y[e] * kLog2e);
-                const int at = 32 * q + i4 + e;
-                if (all) {
-                  acc[e] += v;
-                } else if (at >= lo && at < hi) {
-                  acc[e] += v;
-                }
-              }
+          for (int i4 = 0; i4 < 32; i4 += 4) {
+            const float4 z = *reinterpret_cast<const float4*>(col + 32 * q + i4);  // - lse
+            float2 y0 = make_float2(__uint_as_float(v[i4]), __uint_as_float(v[i4 + 1]));
+            float2 y1 = make_float2(__uint_as_float(v[i4 + 2]), __uint_as_float(v[i4 + 3]));
+            if constexpr (FORM == kFormCap) {
+              y0 = __fadd2_rn(y0, make_float2(z.x, z.y));
+              y1 = __fadd2_rn(y1, make_float2(z.z, z.w));
+            } else {
+              y0 = __ffma2_rn(y0, c2, make_float2(z.x, z.y));
+              y1 = __ffma2_rn(y1, c2, make_float2(z.z, z.w));
             }
+            if (biased) {
+              const float4 sl = *reinterpret_cast<const float4*>(col + kMsCols + 32 * q + i4);
+              const float4 ps = *reinterpret_cast<const float4*>(col + 2 * kMsCols + 32 * q + i4);
+              y0.x = fmaf(-sl.x, fabsf(ps.x - key_f), y0.x);
+              y0.y = fmaf(-sl.y, fabsf(ps.y - key_f), y0.y);
+              y1.x = fmaf(-sl.z, fabsf(ps.z - key_f), y1.x);
+              y1.y = fmaf(-sl.w, fabsf(ps.w - key_f), y1.y);
+            }
+            y0 = __fmul2_rn(y0, k2);
+            y1 = __fmul2_rn(y1, k2);
+            v[i4] = __float_as_uint(ex2(y0.x));
+            v[i4 + 1] = __float_as_uint(ex2(y0.y));
+            v[i4 + 2] = __float_as_uint(ex2(y1.x));
+            v[i4 + 3] = __float_as_uint(ex2(y1.y));
+          }
+          if (!all) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (!(seen & (1u << e))) v[e] = 0u;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            acc[(e / 2) % 4] = __fadd2_rn(acc[(e / 2) % 4], make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
+          }
+        };
+        // A quarter's columns load while the one before is summed; S is free for the next product but
+        // one as soon as the last is in registers.
+        auto done_reading = [&](bool last) {
+          if (!last) return;
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kBarSFree + 2 * x + buf));
+        };
+#pragma unroll 1
+        for (int q = 0; q < quarters; q += 2) {
+          tmem_wait_ld_x32(s[0]);
+          done_reading(q + 1 == quarters);
+          if (q + 1 < quarters) tmem_ld_x32(t_b + 32u * (q + 1), s[1]);
+          add(s[0], q);
+          if (q + 1 < quarters) {
+            tmem_wait_ld_x32(s[1]);
+            done_reading(q + 2 == quarters);
+            if (q + 2 < quarters) tmem_ld_x32(t_b + 32u * (q + 2), s[0]);
+            add(s[1], q + 1);
           }
         }
         __syncwarp();
@@ -570,7 +601,8 @@ __global__ void __launch_bounds__(kMsThreads, 1)
       if (!ok) break;
       if (key < most && (n > 0 || !p.accumulate)) {
         const bool skipped = ((bad >> (r_local >> log2T)) & 1u) != 0;
-        const float sum = skipped ? 0.f : (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        const float2 both = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+        const float sum = skipped ? 0.f : both.x + both.y;
         float* dst = p.mass + (static_cast<size_t>(w.b) * p.s.Hkv + w.kvh) * most + key;
         *dst = p.accumulate ? *dst + sum : sum;
       }
