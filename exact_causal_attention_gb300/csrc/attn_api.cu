@@ -782,11 +782,23 @@ int check_paged_args(const void* cache, const int* block_table, const int* lengt
   return ATTN_OK;
 }
 
-int paged_cache_map(CUtensorMap* map, const void* cache, bool bf16, int D, int Hkv, int T, int P) {
+int cache_group_map(CUtensorMap* map, const void* cache, bool bf16, int D, int Hkv, int T, int P) {
   std::lock_guard<std::mutex> lock(g_mutex);
   EncodeTiledFn encode = nullptr;
   const int rc = get_encode_fn(&encode);
-  return rc != ATTN_OK ? rc : encode_cache_map(encode, map, cache, bf16, D, Hkv, T, P);
+  if (rc != ATTN_OK) return rc;
+  const cuuint64_t row = static_cast<cuuint64_t>(Hkv) * D * 2;  // bytes of a token's K (or V)
+  const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(D / 64),
+                              static_cast<cuuint64_t>(P) * 2 * static_cast<cuuint64_t>(T / 8),
+                              static_cast<cuuint64_t>(Hkv)};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, static_cast<cuuint64_t>(D) * 2};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(T / 8), 1};
+  const cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
+  const CUresult r =
+      encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+             const_cast<void*>(cache), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
 int head_rows_map(CUtensorMap* map, const void* ptr, bool bf16, int D, int H, int R, unsigned box_h, unsigned box_r) {

@@ -34,9 +34,10 @@ uint64_t align256(uint64_t x);
 int check_paged_args(const void* cache, const int* block_table, const int* lengths, int B, int Hkv, int D,
                      int page_size, int max_pages, int num_pages);
 
-// Paged cache [P, 2, T, Hkv, D] as a rank-3 map (D, Hkv, P*2*T): one box is the
-// T x 64 block of one head on one page, 128-byte swizzle.
-int paged_cache_map(CUtensorMap* map, const void* cache, bool bf16, int D, int Hkv, int T, int P);
+// Paged cache [P, 2, T, Hkv, D] in groups of 8 tokens, as a rank-5 map (64 columns, 8 tokens,
+// D/64 column blocks, P*2*T/8 groups, Hkv): one box is one head's K or V of one page, 128-byte
+// swizzle, in shared memory group by group, column block by column block.
+int cache_group_map(CUtensorMap* map, const void* cache, bool bf16, int D, int Hkv, int T, int P);
 
 // Rows [R, H, D] of 16-bit elements (D contiguous) as a rank-3 map (D, H, R): one box
 // is 64 columns of box_h heads of box_r rows, 128-byte swizzle; heads fastest in

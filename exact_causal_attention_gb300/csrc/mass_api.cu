@@ -64,13 +64,14 @@ int mass_impl(bool bf16, const void* q, const float* lse, const void* cache, con
   p.small_plan = eca::line_is_small(
       B, static_cast<double>(B) * ((static_cast<double>(max_pages) * page_size) / eca::kMsTile + 1));
   p.by_hc = eca::make_fast_div(p.hc);
+  p.by_tq = eca::make_fast_div(p.tq);
   p.wait_limit_ns = kWaitLimitNs;
   p.timeout_code = ATTN_ERR_TIMEOUT;
   CUtensorMap tm_q, tm_cache;
   // Without rows nothing reads the queries' map.
   rc = head_rows_map(&tm_q, total_q > 0 ? q : cache, bf16, D, Hq, total_q > 0 ? total_q : 1,
                      static_cast<unsigned>(p.hc), static_cast<unsigned>(p.tq));
-  if (rc == ATTN_OK) rc = paged_cache_map(&tm_cache, cache, bf16, D, Hkv, page_size, num_pages);
+  if (rc == ATTN_OK) rc = cache_group_map(&tm_cache, cache, bf16, D, Hkv, page_size, num_pages);
   if (rc != ATTN_OK) return rc;
   const uint64_t tiles = static_cast<uint64_t>(B) * Hkv *
                          ((static_cast<uint64_t>(max_pages) * page_size + eca::kMsTile - 1) / eca::kMsTile);

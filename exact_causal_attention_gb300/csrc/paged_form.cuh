@@ -20,7 +20,7 @@ struct CapScale {
   float in;     // scale / cap
   float out;    // cap unit
   float limit;  // |x| up to which the polynomial holds
-  float c[8];   // its coefficients for x^2, with the scales folded in
+  float2 c[8];  // its coefficients for x^2, with the scales folded in, for pairs of scores
 };
 
 __device__ __forceinline__ CapScale cap_scale(float scale, float softcap, float unit) {
@@ -34,7 +34,7 @@ __device__ __forceinline__ CapScale cap_scale(float scale, float softcap, float 
   float f = r.out * r.in;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    r.c[i] = kCoef[i] * f;
+    r.c[i] = make_float2(kCoef[i] * f, kCoef[i] * f);
     f *= r.in * r.in;
   }
   return r;
@@ -57,9 +57,9 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k)
     for (int i = 0; i < 32; i += 2) {
       const float2 x = make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
       const float2 z = __fmul2_rn(x, x);
-      float2 a = make_float2(k.c[7], k.c[7]);
+      float2 a = k.c[7];
 #pragma unroll
-      for (int j = 6; j >= 0; --j) a = __ffma2_rn(a, z, make_float2(k.c[j], k.c[j]));
+      for (int j = 6; j >= 0; --j) a = __ffma2_rn(a, z, k.c[j]);
       a = __fmul2_rn(a, x);
       s[i] = __float_as_uint(a.x);
       s[i + 1] = __float_as_uint(a.y);

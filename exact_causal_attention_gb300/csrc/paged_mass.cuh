@@ -46,7 +46,7 @@ struct MassParams {
   int tq;             // tokens per step
   int small_plan;     // the line is laid out by one warp
   uint32_t idesc;     // of the MMA: 128 x (hc tq rounded up to 16)
-  FastDiv by_hc;
+  FastDiv by_hc, by_tq;
   unsigned long long wait_limit_ns;
   int timeout_code;
 };
@@ -92,13 +92,13 @@ struct TileSteps {
 __device__ __forceinline__ TileSteps tile_steps(const MassParams& p, int n, int pos0, int prefix, int len, int kt) {
   const int kb = kt * kMsTile;
   if (kb >= len || n == 0) return TileSteps{0, 0};
-  if (kb < prefix) return TileSteps{0, (n + p.tq - 1) / p.tq};
+  if (kb < prefix) return TileSteps{0, fast_div(n - 1, p.by_tq) + 1};
   const int lo = max(0, kb - pos0);
   const int hi = p.f.window > 0 ? static_cast<int>(min(static_cast<long long>(n),
                                                        static_cast<long long>(kb) + kMsTile - 1 + p.f.window - pos0))
                                 : n;
   if (lo >= hi) return TileSteps{0, 0};
-  return TileSteps{lo / p.tq, (hi + p.tq - 1) / p.tq};
+  return TileSteps{fast_div(lo, p.by_tq), fast_div(hi - 1, p.by_tq) + 1};
 }
 
 // Two key tiles (or one) of one (request, head).
@@ -234,24 +234,23 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     const uint64_t pol = policy_evict_first();
     int it = 0, pushed = 0;
     bool ok = true;
+    PageWalk walk;
+    walk.step = 1;
+    walk.log2T = log2T;
+    walk.num_pages = p.s.num_pages;
     int b = from.b, head = from.head, tile = from.tile;
     while (ok && b < B && b <= to.b) {
       const Request r = load_request(p.s, &p.f, b);
       const int n_items = items_of(r.n, r.len);
       const int* table = p.s.block_table + static_cast<size_t>(b) * p.s.max_pages;
       // The window reaches down to the first token's.
-      const int w0 = p.f.window > 0 ? max(0, r.pos0 - p.f.window + 1) : 0;
-      auto page_of = [&](int kt, bool* needed) -> int {
-        const int pg = kt * pages + lane;
-        const int tok = pg << log2T;
-        *needed = lane < pages && kt < n_items && tok < r.len && (tok < r.prefix || tok + T > w0);
-        return *needed ? table[pg] : 0;
-      };
+      walk.from0 = p.f.window > 0 ? max(0, r.pos0 - p.f.window + 1) : 0;
+      walk.to0 = r.len;
+      walk.prefix = r.prefix;
       for (; ok && head < p.s.Hkv && n_items > 0; ++head, tile = 0) {
         const bool last = b == to.b && head == to.head;
         const int stop = last ? min(to.tile, n_items) : n_items;
-        bool needed;
-        int id = page_of(tile, &needed);
+        if (tile < stop) walk.start(table, tile * pages >> 5);
         while (ok && tile < stop) {
           const TileSteps s0 = tile_steps(p, r.n, r.pos0, r.prefix, r.len, tile);
           TileSteps s1 = {0, 0};
@@ -285,13 +284,8 @@ __global__ void __launch_bounds__(kMsThreads, 1)
           }
           ++pushed;
           for (int x = 0; x < (two ? 2 : 1); ++x) {
-            const bool good = needed && id >= 0 && id < p.s.num_pages;
-            const bool load = needed;
-            const int my_id = id;
-            id = page_of(tile + x + 1, &needed);  // the next tile's ids are on their way while this one loads
             if (!seen) continue;
-            const uint32_t bad = __ballot_sync(0xffffffffu, load && !good);
-            if (load && !good) atomicExch(p.s.status, p.s.bad_index_code);
+            const int at = walk.hold((tile + x) * pages, p.s.status, p.s.bad_index_code);
             const int slot = it % L::kKStages;
             if (!__all_sync(0xffffffffu, wd.wait(bar(L::kBarKEmpty + slot), parity(it / L::kKStages) ^ 1u))) {
               ok = false;
@@ -299,17 +293,14 @@ __global__ void __launch_bounds__(kMsThreads, 1)
             }
             const uint32_t full = bar(L::kBarKFull + slot);
             if (lane == 0) {
-              bad_pages[it % kMsBadRing] = bad;
+              bad_pages[it % kMsBadRing] = (walk.bad >> at) & ((1u << pages) - 1u);
               mbar_arrive_expect_tx(full, L::kTileBytes);
             }
             __syncwarp();
-            if (lane < pages) {
-              const uint32_t dst = sbase + L::kKOff + slot * L::kTileBytes + (lane << log2T) * 128;
-              const int z = good ? my_id * 2 * T : p.s.num_pages * 2 * T;  // out of range: zeros
-#pragma unroll
-              for (int s = 0; s < L::kSub; ++s) {
-                tma_load_3d(dst + s * kSubTileBytes, &tm_cache, full, 64 * s, head, z, pol);
-              }
+            uint32_t dst = sbase + L::kKOff + slot * L::kTileBytes;
+#pragma unroll 2
+            for (int i = 0; i < pages; ++i, dst += T * 2 * D) {
+              tma_load_page(dst, &tm_cache, full, __shfl_sync(0xffffffffu, walk.z, at + i), head, pol);
             }
             ++it;
           }
@@ -335,7 +326,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------ MMA issuer
-    const uint64_t k_desc = smem_desc_sw128(sbase + L::kKOff, 16, 1024);
+    const uint64_t k_desc = TileLayout<D>::k_desc(sbase + L::kKOff);
     const uint64_t q_desc = smem_desc_sw128(sbase + L::kQOff, 16, 1024);
     auto warp_wait = [&](uint32_t b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, wd.wait(b, ph)) != 0; };
     int it = 0, step = 0;
@@ -370,8 +361,9 @@ __global__ void __launch_bounds__(kMsThreads, 1)
           const uint64_t bq = q_desc + static_cast<uint64_t>(qs * (L::kTileBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = static_cast<uint64_t>((kk / 4) * (kSubTileBytes >> 4) + (kk % 4) * 2);
-            mma_ss_warp(tmem + 256u * x + 128u * buf, a + off, bq + off, p.idesc, kk > 0 ? 1u : 0u);
+            mma_ss_warp(tmem + 256u * x + 128u * buf, a + TileLayout<D>::k_step(kk),
+                        bq + static_cast<uint64_t>((kk / 4) * (kSubTileBytes >> 4) + (kk % 4) * 2), p.idesc,
+                        kk > 0 ? 1u : 0u);
           }
           tc_commit_warp(bar(L::kBarS + 2 * x + buf));
         }

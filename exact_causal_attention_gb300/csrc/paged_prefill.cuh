@@ -21,8 +21,7 @@
 // Inside a CTA (384 threads), as in the dense kernel: warps 0-3 and 4-7 softmax of query tiles 0 and
 // 1 (one row per thread = one TMEM lane), warp 8 producer (page ids, TMA of K and V), warps 9 and 10
 // one MMA issuer per query tile, passing a turn token, warp 11 TMA loads of Q.  K and V tiles alternate
-// in one ring of shared memory, each assembled from the tile's pages (T x 64 boxes with the 128-byte
-// swizzle).  TMEM: S_t at column 128 t, O_t at 256 + D t, P_t over S_t.
+// in one ring of shared memory, each assembled from the tile's pages, one copy per page (TileLayout).  TMEM: S_t at column 128 t, O_t at 256 + D t, P_t over S_t.
 //
 // Masks.  Key tiles that no row of the unit sees are skipped (a window leaves a gap between the
 // prefix and the window).  In a tile that some row sees in part, hidden scores become -inf before
@@ -161,6 +160,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_cache,
                          const PrefillParams p) {
   using L = PrefillSmem<D>;
+  using Tile = TileLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;
@@ -259,29 +259,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   } else {
     __syncwarp();
   }
-  // The unit that starts here and ends in a later CTA: for the combine kernel.
-  if (warp == 8 && lane == 0) {
-    int parts = 0;
-    int* split = p.split + cta * kPfSplitWords;
-    if (has_work && to.b < B && to.tile > 0 && to.tile < to.k) {
-      const bool started_before = from.b == to.b && from.head == to.head && from.pair == to.pair && from.tile > 0;
-      if (!started_before) {
-        parts = 2;
-        for (int c = cta + 2; c < G; ++c) {
-          const long long y = line_cut(W, G, c) - to.start;
-          if (y >= to.k + kPfUnitCost || cut_tile(y, to.k) >= to.k) break;
-          ++parts;
-        }
-        const Request r = load_request(p.s, &p.f, to.b);
-        const PairTiles u = pair_tiles(p, r.n, r.pos0, r.prefix, to.pair);
-        split[1] = r.row0 + u.tok0;
-        split[2] = u.n0 + u.n1;
-        split[3] = to.head * p.hc;
-      }
-    }
-    split[0] = parts;
-  }
-
   // --------------------------------------------------------------------- the roles
   int frags_read = 0;
   // Next fragment for a role (a whole warp, or lane 0 alone): false when a wait gave up.
@@ -308,7 +285,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     setmaxnreg_dec<kRegsControl>();
     if (warp == 8) {
       // ---------------------------------------------------------------- producer
-      // The whole warp: lane i holds the i-th page of a key tile.
       const int T = p.s.page_size;
       const int log2T = 31 - __clz(T);
       const int pages = kPfTile >> log2T;
@@ -317,6 +293,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       Request r = {};
       int b = from.b, head = from.head, pair = from.pair, tile = from.tile;
       int loaded = -1;  // request that r describes
+      PageWalk walk;
+      walk.step = -1;
+      walk.log2T = log2T;
+      walk.num_pages = p.s.num_pages;
       const int end_b = has_work ? to.b : -1;
       auto push = [&](const Fragment& w) -> bool {
         const int q = pushed % kPfQueue;
@@ -376,26 +356,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             ok = false;
             break;
           }
-          // K and V tiles of the fragment, alternating.  The next tile's page ids are read
-          // while this one's copies are issued.
+          // K and V tiles of the fragment, alternating.
           const int kvh = head / p.chunks;
           const int* table = p.s.block_table + static_cast<size_t>(b) * p.s.max_pages;
           // K/V that several units read stays in L2; a lone pair's is read once.
           const uint64_t pol = r.n > per_pair ? policy_evict_last() : policy_evict_first();
-          auto page_of = [&](int j, bool* needed) -> int {
+          auto first_page = [&](int j) -> int {  // of the j-th tile
             const int v = tile + w.n_max - 1 - j;
-            const int pg = (v < u.pre ? v : v + u.gap) * pages + lane;
-            const int tok = pg << log2T;
-            *needed = lane < pages && j < w.n_max && (tok < r.prefix || (tok + T > u.w0 && tok < u.hi));
-            return *needed ? table[pg] : 0;
+            return (v < u.pre ? v : v + u.gap) * pages;
           };
-          bool needed;
-          int id = page_of(0, &needed);
+          walk.from0 = u.w0;
+          walk.to0 = u.hi;
+          walk.prefix = r.prefix;
+          if (w.n_max > 0) walk.start(table, first_page(0) >> 5);
           for (int j = 0; ok && j < w.n_max; ++j) {
-            const bool good = needed && id >= 0 && id < p.s.num_pages;
-            const uint32_t bad = __ballot_sync(0xffffffffu, needed && !good);
-            if (needed && !good) atomicExch(p.s.status, p.s.bad_index_code);
-            const int z = good ? id * 2 * T : p.s.num_pages * 2 * T;  // out of range: zeros
+            const int at = walk.hold(first_page(j), p.s.status, p.s.bad_index_code);
             for (int kind = 0; kind < 2; ++kind) {
               const int slot = it % L::kStages;
               if (!__all_sync(0xffffffffu, wd.wait(bar(L::kBarEmpty + slot), parity(it / L::kStages) ^ 1u))) {
@@ -404,19 +379,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               }
               const uint32_t full = bar(L::kBarFull + slot);
               if (lane == 0) {
-                if (kind == 0) bad_pages[it / 2 % kPfBadRing] = bad;
+                if (kind == 0) bad_pages[it / 2 % kPfBadRing] = (walk.bad >> at) & ((1u << pages) - 1u);
                 mbar_arrive_expect_tx(full, L::kTileBytes);
               }
               __syncwarp();
-              if (lane < pages) {
-                const uint32_t dst = sbase + L::kRingOff + slot * L::kTileBytes + (lane << log2T) * 128;
-#pragma unroll
-                for (int s = 0; s < L::kSub; ++s) {
-                  tma_load_3d(dst + s * kSubTileBytes, &tm_cache, full, 64 * s, kvh, good ? z + kind * T : z, pol);
-                }
+              uint32_t dst = sbase + L::kRingOff + slot * L::kTileBytes;
+#pragma unroll 2
+              for (int i = 0; i < pages; ++i, dst += T * 2 * D) {
+                const int z = __shfl_sync(0xffffffffu, walk.z, at + i) + kind * (T >> 3);
+                tma_load_page(dst, &tm_cache, full, z, kvh, pol);
               }
               ++it;
-              if (kind == 0) id = page_of(j + 1, &needed);
             }
           }
         }
@@ -434,6 +407,28 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         Fragment w = {};
         w.n_max = -1;
         push(w);
+      }
+      // The unit that starts here and ends in a later CTA: for the combine kernel.
+      if (lane == 0) {
+        int parts = 0;
+        int* split = p.split + cta * kPfSplitWords;
+        if (has_work && to.b < B && to.tile > 0 && to.tile < to.k) {
+          const bool started_before = from.b == to.b && from.head == to.head && from.pair == to.pair && from.tile > 0;
+          if (!started_before) {
+            parts = 2;
+            for (int c = cta + 2; c < G; ++c) {
+              const long long y = line_cut(W, G, c) - to.start;
+              if (y >= to.k + kPfUnitCost || cut_tile(y, to.k) >= to.k) break;
+              ++parts;
+            }
+            const Request r = load_request(p.s, &p.f, to.b);
+            const PairTiles u = pair_tiles(p, r.n, r.pos0, r.prefix, to.pair);
+            split[1] = r.row0 + u.tok0;
+            split[2] = u.n0 + u.n1;
+            split[3] = to.head * p.hc;
+          }
+        }
+        split[0] = parts;
       }
       // Let every copy this warp started land before the block can exit.
       for (int x = (it > L::kStages ? it - L::kStages : 0); x < it; ++x) {
@@ -472,9 +467,26 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const uint32_t s_tmem = tmem + 128u * t;
       const uint32_t o_tmem = tmem + 256u + static_cast<uint32_t>(D) * t;
       const uint64_t q_desc = smem_desc_sw128(sbase + L::kQOff + t * L::kTileBytes, 16, 1024);
-      const uint64_t k_desc = smem_desc_sw128(sbase + L::kRingOff, 16, 1024);
-      const uint64_t v_desc = smem_desc_sw128(sbase + L::kRingOff, kSubTileBytes, 1024);
+      const uint64_t k_desc = Tile::k_desc(sbase + L::kRingOff);
+      const uint64_t v_desc = Tile::v_desc(sbase + L::kRingOff);
       auto stage_off = [&](int item) { return static_cast<uint64_t>((item % L::kStages) * (L::kTileBytes >> 4)); };
+      // S_t = Q K^T, and O_t (+)= P V of keys 16 k0 .. 16 k1 - 1.
+      auto qk = [&](int item) {
+        constexpr uint32_t idesc = idesc_f16_f32acc(kBlockM, kBlockN, BF16, false);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          mma_ss_warp(s_tmem, q_desc + static_cast<uint64_t>((kk / 4) * (kSubTileBytes >> 4) + (kk % 4) * 2),
+                      k_desc + stage_off(item) + Tile::k_step(kk), idesc, kk > 0 ? 1u : 0u);
+        }
+      };
+      auto pv = [&](int item, bool accumulate, int k0, int k1) {
+        constexpr uint32_t idesc = idesc_f16_f32acc(kBlockM, D, BF16, true);
+#pragma unroll
+        for (int kk = k0; kk < k1; ++kk) {
+          mma_ts_warp(o_tmem, s_tmem + kk * 8, v_desc + stage_off(item) + Tile::v_step(kk), idesc,
+                      (accumulate || kk > 0) ? 1u : 0u);
+        }
+      };
       auto warp_wait = [&](uint32_t b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, wd.wait(b, ph)) != 0; };
       auto item_wait = [&](int x) -> bool { return warp_wait(bar(L::kBarFull + x % L::kStages), parity(x / L::kStages)); };
       int turns = 0;
@@ -498,7 +510,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if ((n_kv > 0 && !warp_wait(bar(L::kBarQFull + t), parity(used))) || !item_wait(it)) break;
         tc_fence_after_sync();
         if (!take_turn()) break;
-        if (first == 0) issue_qk<D, BF16>(s_tmem, q_desc, k_desc + stage_off(it));
+        if (first == 0) qk(it);
         pass_turn();
         if (first == 0) {
           tc_commit_warp(bar(L::kBarS + t));
@@ -529,13 +541,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             break;
           }
           if (j >= first) {
-            issue_pv<D, BF16>(o_tmem, s_tmem, v_desc + stage_off(xv), j > first, 0, 4);
+            pv(xv, j > first, 0, 4);
             if (!warp_wait(bar(L::kBarPb + t), parity(p_waits - 1))) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
-            issue_pv<D, BF16>(o_tmem, s_tmem, v_desc + stage_off(xv), true, 4, 8);
+            pv(xv, true, 4, 8);
           }
           if (j + 1 < w.n_max) {
             if (!item_wait(xk)) {
@@ -544,7 +556,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             if (j + 1 >= first) {
               tc_fence_after_sync();
-              issue_qk<D, BF16>(s_tmem, q_desc, k_desc + stage_off(xk));
+              qk(xk);
             }
           }
           pass_turn();
@@ -630,7 +642,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const uint32_t base = sbase + L::kRingOff + (x % L::kStages) * L::kTileBytes;
           for (int i = r_local; i < (z1 - z0) * L::kSub * 8; i += 128) {
             const int row = z0 + i / (L::kSub * 8), at = i % (L::kSub * 8);
-            st_shared_v4(base + (at / 8) * kSubTileBytes + row * 128 + (at % 8) * 16, 0u, 0u, 0u, 0u);
+            st_shared_v4(base + Tile::row(row, at / 8) + (at % 8) * 16, 0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
           return true;

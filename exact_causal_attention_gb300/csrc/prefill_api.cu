@@ -100,7 +100,7 @@ int prefill_impl(bool bf16, const void* q, const void* cache, const int* block_t
   p.timeout_code = ATTN_ERR_TIMEOUT;
   CUtensorMap tm_q, tm_cache;
   rc = head_rows_map(&tm_q, q, bf16, D, Hq, total_q, static_cast<unsigned>(sh.hc), static_cast<unsigned>(sh.tq));
-  if (rc == ATTN_OK) rc = paged_cache_map(&tm_cache, cache, bf16, D, Hkv, page_size, num_pages);
+  if (rc == ATTN_OK) rc = cache_group_map(&tm_cache, cache, bf16, D, Hkv, page_size, num_pages);
   if (rc != ATTN_OK) return rc;
   const int grid = sh.grid < dev.sm_count ? sh.grid : dev.sm_count;  // one CTA per SM
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
