@@ -80,6 +80,7 @@ CACHE_SIGNATURES = {
     "attn_paged_evict": (_I, [_VP] * 7 + [_I] * 2 + _PAGES + [_I, _I, _VP]),
     "attn_decode_paged_form": (_I, _DECODE_FORM),
     "attn_decode_paged_form_bf16": (_I, _DECODE_FORM),
+    "attn_decode_form_default_splits": (_I, [_I] * 5),
 }
 
 
@@ -428,7 +429,8 @@ def decode_paged(q, cache, block_table, lengths, scale: float | None = None, kv_
         slopes, prefix = _form_ptrs(alibi_slopes, prefix_lens, Hq, B, dev)
     with _on_device(dev):
         if kv_splits is None:
-            kv_splits = lib.attn_decode_default_splits(B, Hq, Hkv, T, max_pages)
+            pick = lib.attn_decode_form_default_splits if form else lib.attn_decode_default_splits
+            kv_splits = pick(B, Hq, Hkv, T, max_pages)
             if kv_splits < 0:
                 raise AttnError(kv_splits, "attn_decode_default_splits")
         if out is None:

@@ -611,7 +611,12 @@ template <int D, bool BF16, bool FORM>
 int launch_decode(const CUtensorMap& tm, eca::DecodeParams& p, const DecodeShape& sh, DeviceState* st,
                   cudaStream_t stream) {
   using L = eca::DecodeSmem<D>;
-  const long long ctas = static_cast<long long>(p.B) * p.Hkv * sh.head_chunks * sh.splits;
+  const long long groups = static_cast<long long>(p.B) * p.Hkv * sh.head_chunks;
+  long long ctas = groups * sh.splits;
+  if (FORM) {
+    // Segments of one size for all requests: rounding up adds at most one CTA per group.
+    if (ctas > p.target + groups) ctas = p.target + groups;
+  }
   if (ctas > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   const unsigned grid = static_cast<unsigned>(ctas);
   auto run = [&](auto kernel, unsigned bit) -> int {
@@ -714,6 +719,7 @@ int decode_impl(bool bf16, const void* q, const void* cache, const int* block_ta
   p.slopes = slopes;
   p.prefix = prefix;
   p.window = window;
+  p.target = 3 * st->sm_count;  // as many as run at once
   // A prefix changes nothing where every token is visible.
   const bool form = softcap > 0.f || window > 0 || slopes != nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -955,6 +961,18 @@ int attn_decode_default_splits(int B, int Hq, int Hkv, int page_size, int max_pa
   if (s > tiles) s = tiles;
   if (s > kMaxSplits) s = kMaxSplits;
   return s < 1 ? 1 : static_cast<int>(s);
+}
+
+int attn_decode_form_default_splits(int B, int Hq, int Hkv, int page_size, int max_pages) {
+  const int even = attn_decode_default_splits(B, Hq, Hkv, page_size, max_pages);
+  if (even < 0) return even;
+  // The segments are of one size, so a request longer than the mean gets more than the mean number;
+  // a few times that many keep the longest from setting the time.
+  const long long tiles = (static_cast<long long>(max_pages) * page_size + eca::kDecTile - 1) / eca::kDecTile;
+  long long s = 6LL * even < 8 ? 8 : 6LL * even;
+  if (s > tiles) s = tiles;
+  if (s > kMaxSplits) s = kMaxSplits;
+  return static_cast<int>(s);
 }
 
 int attn_paged_append(const void* new_kv, void* cache, const int* block_table, const int* lengths, int B, int Hkv,

@@ -62,7 +62,7 @@ int mass_impl(bool bf16, const void* q, const float* lse, const void* cache, con
   if (p.tq > mean) p.tq = mean > 0 ? mean : 1;
   p.idesc = eca::idesc_f16_f32acc(eca::kMsTile, (p.hc * p.tq + 15) / 16 * 16, bf16, false);
   p.small_plan = eca::line_is_small(
-      B, static_cast<double>(B) * ((static_cast<double>(max_pages) * page_size) / eca::kMsTile + 1));
+      B, static_cast<double>(B) * ((static_cast<double>(max_pages) * page_size) / (2 * eca::kMsTile) + 1));
   p.by_hc = eca::make_fast_div(p.hc);
   p.by_tq = eca::make_fast_div(p.tq);
   p.wait_limit_ns = kWaitLimitNs;

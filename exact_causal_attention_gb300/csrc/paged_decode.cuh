@@ -69,6 +69,7 @@ struct DecodeParams {
   const float* slopes;  // [Hq] or null
   const int* prefix;    // [B] or null
   int window;           // 0: none
+  int target;           // CTAs to cut the contexts for
 };
 
 // Visible pages of one request under the FORM instances: logical pages 0 .. pre - 1
@@ -79,7 +80,6 @@ struct DecodePages {
   int pre, gap;
   int lo;       // first token of the window
   int prefix;   // tokens of the prefix
-  int seg_pages;  // pages of one segment: the visible pages shared out evenly, whole tiles
   __device__ __forceinline__ int logical(int v) const { return v < pre ? v : v + gap; }
 };
 
@@ -92,10 +92,39 @@ __device__ __forceinline__ DecodePages decode_pages(const DecodeParams& p, int b
   d.pre = (d.prefix + T - 1) >> log2T;
   d.gap = max(0, (d.lo >> log2T) - d.pre);
   d.n = n_pages - d.gap;
-  const int per_tile = kDecTile >> log2T;
-  const int seg = (d.n + p.splits - 1) / p.splits;
-  d.seg_pages = max(1, (seg + per_tile - 1) / per_tile) * per_tile;
   return d;
+}
+
+// The request's length, at the nearest end when it is out of range.
+__device__ __forceinline__ int decode_length(const DecodeParams& p, int b) {
+  return min(max(p.lengths[b], 0), p.max_pages * p.page_size);
+}
+
+// How the FORM instances cut the contexts into segments: all of one size (in tiles of
+// kDecTile tokens), so that a long request gets more of them than a short one and every CTA about the
+// same work.  About p.target CTAs in all, and no more than p.splits segments a request.
+// Called by a whole warp, which reads every length (32 at a time).
+struct DecodeCut {
+  int tiles;  // of a segment
+};
+
+__device__ __forceinline__ int decode_tiles(const DecodeParams& p, int b, int log2T) {
+  const int per_tile = kDecTile >> log2T;
+  return (decode_pages(p, b, decode_length(p, b), log2T).n + per_tile - 1) / per_tile;
+}
+
+__device__ __forceinline__ DecodeCut decode_cut(const DecodeParams& p, int log2T) {
+  long long total = 0;
+  int most = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + static_cast<int>(threadIdx.x % 32);
+    const int t = b < p.B ? decode_tiles(p, b, log2T) : 0;
+    most = max(most, __reduce_max_sync(0xffffffffu, t));
+    total += __reduce_add_sync(0xffffffffu, t);
+  }
+  const long long even = (total * p.Hkv * p.head_chunks + p.target - 1) / p.target;
+  const int least = (most + p.splits - 1) / p.splits;
+  return DecodeCut{max(1, max(static_cast<int>(even), least))};
 }
 
 // Bits 0 .. n - 1.
@@ -196,14 +225,49 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
   if (threadIdx.x == kDecWarps * 32) tma_prefetch_map(&tm_cache);
   grid_dependency_wait();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  // unit: (b, kv head, head chunk, segment), segment fastest
   int u = blockIdx.x;
-  const int seg = u % p.splits;
-  u /= p.splits;
-  const int chunk = u % p.head_chunks;
-  u /= p.head_chunks;
-  const int kvh = u % p.Hkv;
-  const int b = u / p.Hkv;
+  int seg, chunk, kvh, b;
+  int seg_tiles = 0;  // FORM
+  if constexpr (FORM) {
+    // unit: (b, segment, kv head, head chunk), the heads of a segment (contiguous in memory) side by side
+    const int form_log2T = 31 - __clz(p.page_size);
+    seg_tiles = decode_cut(p, form_log2T).tiles;
+    const int heads = p.Hkv * p.head_chunks;
+    b = p.B;
+    int before = 0;  // CTAs of the requests before
+    for (int b0 = 0; b0 < p.B && b == p.B; b0 += 32) {
+      const int mine = b0 + lane;
+      // An empty request has one segment, which writes its output.
+      const int n = mine < p.B ? max(1, (decode_tiles(p, mine, form_log2T) + seg_tiles - 1) / seg_tiles) * heads : 0;
+      int upto = n;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int up = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += up;
+      }
+      const unsigned here = __ballot_sync(0xffffffffu, n > 0 && u < before + upto);
+      if (here != 0) {
+        const int src = __ffs(here) - 1;
+        b = b0 + src;
+        u -= before + __shfl_sync(0xffffffffu, upto - n, src);
+      } else {
+        before += __shfl_sync(0xffffffffu, upto, 31);
+      }
+    }
+    if (b == p.B) return;  // the grid is an upper bound
+    seg = u / heads;
+    u -= seg * heads;
+    chunk = u % p.head_chunks;
+    kvh = u / p.head_chunks;
+  } else {
+    // unit: (b, kv head, head chunk, segment), segment fastest
+    seg = u % p.splits;
+    u /= p.splits;
+    chunk = u % p.head_chunks;
+    u /= p.head_chunks;
+    kvh = u % p.Hkv;
+    b = u / p.Hkv;
+  }
   const int group = p.Hq / p.Hkv;
   const int qh0 = kvh * group + chunk * HC;  // first query head of this CTA
   const int T = p.page_size;
@@ -227,9 +291,9 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
   DecodePages vis = {};
   if constexpr (FORM) {
     vis = decode_pages(p, b, len, log2T);
-    pg_begin = seg * vis.seg_pages;
+    pg_begin = seg * seg_tiles * pages_per_tile;
   }
-  auto seg_pages = [&]() { return FORM ? vis.seg_pages : p.seg_pages; };
+  auto seg_pages = [&]() { return FORM ? seg_tiles * pages_per_tile : p.seg_pages; };
   const int n_pages = FORM ? vis.n : (len + T - 1) >> log2T;
   const int pg_end = min(n_pages, pg_begin + seg_pages());
   if constexpr (FORM) {
@@ -536,7 +600,8 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
     __syncthreads();  // this segment's partial results are written
     if (tid == 0) {
       __threadfence();
-      unsigned* counter = p.counters + static_cast<size_t>(blockIdx.x / p.splits);
+      unsigned* counter = p.counters + (FORM ? static_cast<size_t>(b * p.Hkv + kvh) * p.head_chunks + chunk
+                                             : static_cast<size_t>(blockIdx.x / p.splits));
       const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(valid - 1);
       if (last) {
         *counter = 0u;  // back to zero for the next launch
@@ -615,9 +680,9 @@ __global__ void __launch_bounds__(256) paged_decode_combine(const DecodeParams p
     int n_pages = (len + p.page_size - 1) / p.page_size;
     int seg_pages = p.seg_pages;
     if constexpr (FORM) {
-      const DecodePages vis = decode_pages(p, b, len, 31 - __clz(p.page_size));
-      n_pages = vis.n;
-      seg_pages = vis.seg_pages;
+      const int log2T = 31 - __clz(p.page_size);
+      n_pages = decode_pages(p, b, len, log2T).n;
+      seg_pages = decode_cut(p, log2T).tiles * (kDecTile >> log2T);
     }
     const int valid = min(p.splits, (n_pages + seg_pages - 1) / seg_pages);
     const size_t stride = static_cast<size_t>(p.B) * p.Hq;

@@ -7,8 +7,9 @@
 // For one decode step a key tile meets one step of g columns and the kernel is bound by reading K;
 // for a chunk it is bound by the exponentials, one per (pair, key).
 //
-// A CTA takes an equal part of the line of key tiles (paged_plan.cuh), two tiles of one
-// (request, head) at a time, one per slot; their steps of queries stream through a ring that both share.
+// A CTA takes an equal part of the line of units (paged_plan.cuh): two consecutive key tiles of one
+// (request, head), one per slot, with the heads of a pair of tiles side by side, as they lie in
+// memory (a token's heads are contiguous).  The queries' steps stream through a ring that both slots share.
 // 384 threads: warps 0-3 and 4-7 sum slots 0 and 1, warp 8 produces key tiles from their pages, warp 9
 // issues the MMAs, warp 10 loads Q, warp 11 the columns' log-sum-exps (and slopes and positions).  S^T is
 // double-buffered per slot and read whole into registers, so the next product never waits for the sums.
@@ -27,7 +28,7 @@ namespace eca {
 constexpr int kMsThreads = 384;
 constexpr int kMsTile = 128;       // keys per tile
 constexpr int kMsCols = 128;       // most columns of a step
-constexpr int kMsTileCost = 2;     // a key tile's own cost, in steps
+constexpr int kMsPairCost = 2;     // a pair of key tiles' own cost, in steps
 constexpr int kMsQueue = 4;
 constexpr int kMsReaders = 11;
 constexpr int kMsColStages = 4;    // ring of the columns' values
@@ -172,12 +173,20 @@ __global__ void __launch_bounds__(kMsThreads, 1)
   const int B = p.s.B;
   const int most = p.s.max_pages * p.s.page_size;
   const LineTables line = line_tables(smem, reinterpret_cast<long long*>(smem + L::kScanOff));
-  // Written in full, a tile that no row sees is an item too.
-  auto items_of = [&](int n, int len) { return ((p.accumulate ? (n > 0 ? len : 0) : most) + kMsTile - 1) / kMsTile; };
+  // Items are pairs of key tiles; written in full, a pair that no row sees is one too.
+  auto items_of = [&](int n, int len) {
+    return ((p.accumulate ? (n > 0 ? len : 0) : most) + 2 * kMsTile - 1) / (2 * kMsTile);
+  };
   auto items = [&](const int4& r) { return items_of(r.x, r.w); };
+  auto steps_of = [&](int n, int pos0, int prefix, int len, int pair) -> TileSteps {
+    const TileSteps a = tile_steps(p, n, pos0, prefix, len, 2 * pair), b = tile_steps(p, n, pos0, prefix, len, 2 * pair + 1);
+    if (a.q1 == 0) return b;
+    if (b.q1 == 0) return a;
+    return TileSteps{min(a.q0, b.q0), max(a.q1, b.q1)};
+  };
   auto cost = [&](const int4& r, int i) {
-    const TileSteps t = tile_steps(p, r.x, r.y, r.z, r.w, i);
-    return t.q1 > t.q0 ? kMsTileCost + (t.q1 - t.q0) * p.chunks : 1;
+    const TileSteps t = steps_of(r.x, r.y, r.z, r.w, i);
+    return t.q1 > t.q0 ? kMsPairCost + (t.q1 - t.q0) * p.chunks : 1;
   };
   // Only the producer needs the plan; a long one is laid out by the whole block.
   long long W = 0;
@@ -188,13 +197,17 @@ __global__ void __launch_bounds__(kMsThreads, 1)
   }
   const int cta = static_cast<int>(blockIdx.x), G = static_cast<int>(gridDim.x);
   struct Place {
-    int b, head, tile;
+    int b, pair, head;
   };
-  // Whole tiles: a place past a tile's middle cuts behind it (its tile may then be one past the
-  // request's last, the same cut as the next head's tile 0).
+  // Whole units: a place past a unit's middle cuts behind it.
   auto locate = [&](long long x) -> Place {
-    const LinePlace at = line_locate(line, B, x, cost);
-    return Place{at.b, at.head, at.item + (2 * at.in >= at.cost ? 1 : 0)};
+    const LinePlace at = line_locate<true>(line, B, p.s.Hkv, x, cost);
+    Place r{at.b, at.item, at.head + (2 * at.in >= at.cost ? 1 : 0)};
+    if (r.head == p.s.Hkv) {  // (the pair may then be one past the request's last)
+      r.head = 0;
+      ++r.pair;
+    }
+    return r;
   };
   Place from = {B, 0, 0}, to = {B, 0, 0};
   if (warp == 8 && W > 0) {
@@ -238,30 +251,23 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     walk.step = 1;
     walk.log2T = log2T;
     walk.num_pages = p.s.num_pages;
-    int b = from.b, head = from.head, tile = from.tile;
+    int b = from.b, pair = from.pair, head = from.head;
     while (ok && b < B && b <= to.b) {
       const Request r = load_request(p.s, &p.f, b);
       const int n_items = items_of(r.n, r.len);
-      const int* table = p.s.block_table + static_cast<size_t>(b) * p.s.max_pages;
       // The window reaches down to the first token's.
       walk.from0 = p.f.window > 0 ? max(0, r.pos0 - p.f.window + 1) : 0;
       walk.to0 = r.len;
       walk.prefix = r.prefix;
-      for (; ok && head < p.s.Hkv && n_items > 0; ++head, tile = 0) {
-        const bool last = b == to.b && head == to.head;
-        const int stop = last ? min(to.tile, n_items) : n_items;
-        if (tile < stop) walk.start(table, tile * pages >> 5);
-        while (ok && tile < stop) {
-          const TileSteps s0 = tile_steps(p, r.n, r.pos0, r.prefix, r.len, tile);
-          TileSteps s1 = {0, 0};
-          const bool seen = s0.q1 > s0.q0;
-          bool two = tile + 1 < stop;
-          if (two) {
-            s1 = tile_steps(p, r.n, r.pos0, r.prefix, r.len, tile + 1);
-            two = (s1.q1 > s1.q0) == seen;
-          }
-          const int q0 = two ? min(s0.q0, s1.q0) : s0.q0;
-          const int q1 = two ? max(s0.q1, s1.q1) : s0.q1;
+      if (pair < n_items) walk.start(p.s.block_table + static_cast<size_t>(b) * p.s.max_pages, 2 * pair * pages >> 5);
+      for (; ok && pair < n_items; ++pair, head = 0) {
+        const bool last = b == to.b && pair == to.pair;
+        const int stop = last ? to.head : p.s.Hkv;
+        const TileSteps t = steps_of(r.n, r.pos0, r.prefix, r.len, pair);
+        const bool seen = t.q1 > t.q0;
+        // A slot without keys in the context takes no part.
+        const bool two = (2 * pair + 1) * kMsTile < (seen ? r.len : most);
+        for (; ok && head < stop; ++head) {
           const int q = pushed % kMsQueue;
           if (!__all_sync(0xffffffffu, wd.wait(bar(L::kBarUnitFree + q), parity(pushed / kMsQueue) ^ 1u))) {
             ok = false;
@@ -269,9 +275,9 @@ __global__ void __launch_bounds__(kMsThreads, 1)
           }
           if (lane == 0) {
             volatile int* e = queue + q * L::kEntryInts;
-            e[0] = seen ? q1 - q0 : 0;
-            e[1] = q0;
-            e[2] = tile;
+            e[0] = seen ? t.q1 - t.q0 : 0;
+            e[1] = t.q0;
+            e[2] = 2 * pair;
             e[3] = two;
             e[4] = r.row0;
             e[5] = r.n;
@@ -283,9 +289,8 @@ __global__ void __launch_bounds__(kMsThreads, 1)
             mbar_arrive(bar(L::kBarUnitFull + q));
           }
           ++pushed;
-          for (int x = 0; x < (two ? 2 : 1); ++x) {
-            if (!seen) continue;
-            const int at = walk.hold((tile + x) * pages, p.s.status, p.s.bad_index_code);
+          for (int x = 0; seen && x < (two ? 2 : 1); ++x) {
+            const int at = walk.hold((2 * pair + x) * pages, p.s.status, p.s.bad_index_code);
             const int slot = it % L::kKStages;
             if (!__all_sync(0xffffffffu, wd.wait(bar(L::kBarKEmpty + slot), parity(it / L::kKStages) ^ 1u))) {
               ok = false;
@@ -304,7 +309,6 @@ __global__ void __launch_bounds__(kMsThreads, 1)
             }
             ++it;
           }
-          tile += two ? 2 : 1;
         }
         if (last) {
           b = B;  // done
@@ -312,7 +316,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
         }
       }
       ++b;
-      head = tile = 0;
+      pair = head = 0;
     }
     if (ok) {
       const int q = pushed % kMsQueue;
@@ -469,6 +473,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
       const int n = w.steps * p.chunks;
       const int item = it + x;
       if (n > 0) it += 1 + w.two;
+      const int key = (w.kt + x) * kMsTile + r_local;
       if (x > w.two) {
         // No tile for this slot: it still hands the steps' columns back.
         for (int i = 0; i < n; ++i, ++step) {
@@ -480,9 +485,11 @@ __global__ void __launch_bounds__(kMsThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kBarColEmpty + cs));
         }
+        if (ok && !p.accumulate && key < most) {
+          p.mass[(static_cast<size_t>(w.b) * p.s.Hkv + w.kvh) * most + key] = 0.f;  // past the context
+        }
         continue;
       }
-      const int key = (w.kt + x) * kMsTile + r_local;
       const float key_f = static_cast<float>(key);
       // Tokens that see this key: from .. upto - 1 of the request.
       int from_tok = max(0, key - w.pos0), upto = w.n;

@@ -1,6 +1,6 @@
 // Sharing out work whose sizes live on the device.  Every request has items (pairs of query
-// tiles, key tiles) that cost something, each once per head.  Laid end to end
-// (request, head, item) they form a line; every CTA lays it out for itself and takes its
+// tiles, pairs of key tiles) that cost something, each once per head.  Laid end to end
+// (request, head, item, or request, item, head) they form a line; every CTA lays it out for itself and takes its
 // equal part, so that nothing is counted or waited for across CTAs and the parts
 // are the same whenever the sizes are.
 #pragma once
@@ -181,24 +181,29 @@ struct LinePlace {
   long long start;  // of the item, on the line
 };
 
-// Called by a whole warp; x below the line's length.
-template <typename Cost>
-__device__ __forceinline__ LinePlace line_locate(const LineTables& t, int B, long long x, Cost cost) {
+// Called by a whole warp; x below the line's length.  kHeadsInside: a request's items
+// in order, each with all its heads; else its heads in order, each with all items.
+template <bool kHeadsInside, typename Cost>
+__device__ __forceinline__ LinePlace line_locate(const LineTables& t, int B, int heads, long long x, Cost cost) {
   const int lane = threadIdx.x % 32;
   LinePlace r;
   // Requests without items share their base with the next: the last such one has items.
   r.b = last_at_most(t.base, B, x);
   const long long sum = static_cast<long long>(t.cost[r.b]);
   const long long in = x - t.base[r.b];
-  r.head = ((in | sum) >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(sum))
-                                   : static_cast<int>(in / sum);
-  long long rest = in - r.head * sum;
+  long long rest = in;
+  if constexpr (!kHeadsInside) {
+    r.head = ((in | sum) >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(sum))
+                                     : static_cast<int>(in / sum);
+    rest = in - r.head * sum;
+  }
   r.start = x - rest;
   const int4 q = t.req[r.b];
   const int n = t.first[r.b + 1] - t.first[r.b];
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int i = i0 + lane;
-    const int mine = i < n ? cost(q, i) : 0;
+    const int one = i < n ? cost(q, i) : 0;
+    const long long mine = kHeadsInside ? static_cast<long long>(one) * heads : one;
     long long c = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -210,9 +215,15 @@ __device__ __forceinline__ LinePlace line_locate(const LineTables& t, int B, lon
       const int src = __ffs(here) - 1;
       const long long before = __shfl_sync(0xffffffffu, c - mine, src);
       r.item = i0 + src;
-      r.cost = __shfl_sync(0xffffffffu, mine, src);
-      r.in = static_cast<int>(rest - before);
+      r.cost = __shfl_sync(0xffffffffu, one, src);
+      long long at = rest - before;
       r.start += before;
+      if constexpr (kHeadsInside) {
+        r.head = static_cast<int>(at / r.cost);
+        at -= static_cast<long long>(r.head) * r.cost;
+        r.start += static_cast<long long>(r.head) * r.cost;
+      }
+      r.in = static_cast<int>(at);
       return r;
     }
     const long long all = __shfl_sync(0xffffffffu, c, 31);
@@ -220,6 +231,7 @@ __device__ __forceinline__ LinePlace line_locate(const LineTables& t, int B, lon
     r.start += all;
   }
   r.item = n;  // not reached: a request's items cover its stretch
+  r.head = 0;
   r.cost = r.in = 0;
   return r;
 }

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     long long start;  // of the unit, on the line
   };
   auto locate = [&](long long x) -> Place {
-    const LinePlace at = line_locate(line, B, x, cost);
+    const LinePlace at = line_locate<false>(line, B, heads, x, cost);
     const int k = at.cost - kPfUnitCost;
     return Place{at.b, at.head, at.item, cut_tile(at.in, k), k, at.start};
   };

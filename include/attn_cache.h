@@ -145,7 +145,11 @@ int attn_paged_evict(void* cache, const int* block_table, const int* lengths, co
 /*
  * attn_decode_paged_form -- attn_decode_paged with the score forms above (the row of
  * request b stands at position lengths[b] - 1).  With softcap 0, window 0 and NULL
- * slopes and prefixes it is attn_decode_paged.
+ * slopes it is attn_decode_paged.  Here the visible tokens of all requests are cut into
+ * segments of one size, so that requests of unequal lengths finish together:
+ *   kv_splits : the most segments a request may get, 1 .. 64 (see
+ *               attn_decode_form_default_splits); the workspace is attn_decode_paged's
+ *               for that many.
  */
 int attn_decode_paged_form(const void* q, const void* cache, const int* block_table, const int* lengths,
                            void* out, float* lse, int B, int Hq, int Hkv, int D, int page_size, int max_pages,
@@ -159,6 +163,10 @@ int attn_decode_paged_form_bf16(const void* q, const void* cache, const int* blo
                                 int max_pages, int num_pages, float scale, float softcap, int window,
                                 const float* alibi_slopes, const int* prefix_lens, int kv_splits,
                                 void* workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/* A bound on the segments a request gets, for the current device: some times the
+ * mean that fills it.  Negative attn_status on bad sizes or a non-sm_103 device. */
+int attn_decode_form_default_splits(int B, int Hq, int Hkv, int page_size, int max_pages);
 
 #ifdef __cplusplus
 }
