@@ -43,8 +43,8 @@ int attn_paged_evict(void* cache, const int* block_table, const int* lengths, co
   }
   const uint64_t heads = static_cast<uint64_t>(B) * Hkv;
   const uint64_t mass_bytes = heads * max_pages * page_size * 4, kept_bytes = heads * budget * 4;
-  const int parts = 2 * (D / (8 * eca::kMoveSlice));
-  if (heads * parts > 0x7fffffffull || mass_bytes > (1ull << 40)) return ATTN_ERR_INVALID_ARG;
+  const uint64_t movers = heads * 2 * eca::kMoveCluster;
+  if (movers > 0x7fffffffull || mass_bytes > (1ull << 40)) return ATTN_ERR_INVALID_ARG;
   const uint64_t c_bytes = cache_bytes(Hkv, D, page_size, num_pages);
   if (overlaps(kept, kept_bytes, mass, mass_bytes) || overlaps(kept, kept_bytes, cache, c_bytes) ||
       overlaps(mass, mass_bytes, cache, c_bytes)) {
@@ -68,10 +68,26 @@ int attn_paged_evict(void* cache, const int* block_table, const int* lengths, co
   p.budget = budget;
   p.recent = recent;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  rc = launched(launch_pdl(eca::paged_evict_select_kernel, static_cast<unsigned>(heads), eca::kSelThreads, 0, s, p));
+  // Keys in shared memory where every request's fit.
+  const int most = max_pages * page_size;
+  const int smem = most * 4;
+  if (most <= eca::kSelSmemTokens) {
+    static std::atomic<uint64_t> done{0};
+    rc = configure(eca::paged_evict_select_kernel<true>, dev, &done, eca::kSelSmemTokens * 4, 0);
+    if (rc != ATTN_OK) return rc;
+    rc = launched(launch_pdl(eca::paged_evict_select_kernel<true>, static_cast<unsigned>(heads), eca::kSelThreads, smem, s, p));
+  } else {
+    rc = launched(launch_pdl(eca::paged_evict_select_kernel<false>, static_cast<unsigned>(heads), eca::kSelThreads, 0, s, p));
+  }
   if (rc != ATTN_OK) return rc;
-  return launched(
-      launch_pdl(eca::paged_evict_move_kernel, static_cast<unsigned>(heads * parts), eca::kMoveThreads, 0, s, p));
+  auto move = [&](auto kernel, std::atomic<uint64_t>* done) -> int {
+    const int r = configure(kernel, dev, done, eca::kMoveBytes, 0);
+    if (r != ATTN_OK) return r;
+    return launched(
+        launch_pdl(kernel, static_cast<unsigned>(movers), eca::kMoveThreads, static_cast<size_t>(eca::kMoveBytes), s, p));
+  };
+  static std::atomic<uint64_t> done128{0}, done64{0};
+  return D == 128 ? move(eca::paged_evict_move_kernel<128>, &done128) : move(eca::paged_evict_move_kernel<64>, &done64);
 }
 
 }  // extern "C"

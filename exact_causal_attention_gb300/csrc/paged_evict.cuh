@@ -6,12 +6,13 @@
 // Two kernels.  paged_evict_select: one block per (request, head) finds the mass of
 // the last token that is kept by a radix select on the masses' bit patterns (three
 // digits of 11, 11 and 10 bits; a histogram of the tokens that share the digits
-// fixed so far, in shared memory), then walks the tokens in order with a block scan that
-// gives every kept token its new position.  paged_evict_move: the rows move in
-// place.  A kept token's new position never exceeds its old one and both grow
-// together, so a block that walks its rows in order, reading a batch before it writes one,
-// never overwrites a row that it has yet to read; blocks split a row's columns
-// (and K from V), not the rows, so they do not meet.
+// fixed so far, in shared memory), then walks the tokens in order and gives every kept one its new
+// position.  The masses of up to 32K tokens are read once and kept in shared memory as keys.
+// paged_evict_move: the rows move in place.  A kept token's new position never exceeds its old
+// one and both grow together, so a batch of rows in order may be written once it has been
+// read, and never touches a row of a later batch.  A cluster of 8 blocks takes one head's K or V: they
+// read a batch together, meet at the cluster's barrier, and write it.  Bound by HBM for many heads
+// and by the chain position -> page -> row for few.
 #pragma once
 #include "paged_common.cuh"
 
@@ -38,6 +39,10 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_mass(uint32_t k) {
+  return k == 0u ? __uint_as_float(0x7fffffffu) : __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
 // Inclusive sum over the block's threads in order; `ws` holds one value per warp.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* ws, uint32_t* total) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -60,13 +65,21 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* ws, uint32_
   return before + v;
 }
 
+constexpr int kSelCopies = 4;          // of the histogram: lanes of a warp often meet in one bin
+constexpr int kSelSmemTokens = 32768;  // most tokens whose keys are kept in shared memory
+
+// kKeep: every request's keys fit in (dynamic) shared memory, 4 bytes a token.
+template <bool kKeep>
 __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const EvictParams p) {
   static_assert(kSelThreads == 1024, "block_scan reads one sum per warp of a full block");
-  __shared__ uint32_t hist[kSelBins];
+  __shared__ uint32_t hist[kSelCopies][kSelBins];
   __shared__ uint32_t ws[32];
   __shared__ uint32_t chosen[2];  // digit, candidates above it
+  extern __shared__ uint32_t keys[];
   grid_launch_dependents();
+  for (int i = threadIdx.x; i < kSelCopies * kSelBins; i += kSelThreads) (&hist[0][0])[i] = 0;
   grid_dependency_wait();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int b = blockIdx.x / p.s.Hkv;
   const int most = p.s.max_pages * p.s.page_size;
   int len = p.s.lengths[b];
@@ -81,6 +94,16 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
   const int tail = min(p.recent, n_new);
   const int cand = len - tail;        // tokens that compete: 0 .. cand - 1
   uint32_t want = n_new - tail;       // that many of them are kept
+  // Each warp takes a run of tokens.
+  const int run = ((len + 1023) / 1024) * 32;
+  const int begin = min(len, warp * run), end = min(len, begin + run);
+  __syncthreads();
+  if constexpr (kKeep) {
+#pragma unroll 8
+    for (int i = begin + lane; i < end; i += 32) keys[i] = mass_key(mass[i]);
+    __syncwarp();
+  }
+  auto key_at = [&](int i) -> uint32_t { return kKeep ? keys[i] : mass_key(mass[i]); };
   // Keys above `floor_key` are kept, and the first `ties` of those equal to it.
   uint32_t floor_key = 0, ties = 0;
   if (want == static_cast<uint32_t>(cand)) {
@@ -92,16 +115,22 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
     for (int round = 0; round < 3; ++round) {
       const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
       const uint32_t digits = round == 2 ? 0x3ffu : 0x7ffu;
-      for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = threadIdx.x; i < cand; i += kSelThreads) {
-        const uint32_t key = mass_key(mass[i]);
-        if ((key & mask) == floor_key) atomicAdd(&hist[(key >> shift) & digits], 1u);
+      const int stop = min(end, cand);
+#pragma unroll 4
+      for (int i = begin + lane; i < stop; i += 32) {
+        const uint32_t key = key_at(i);
+        if ((key & mask) == floor_key) atomicAdd(&hist[lane % kSelCopies][(key >> shift) & digits], 1u);
       }
       __syncthreads();
       // Bins from the largest digit down: thread t takes digits top - 2 t and the next.
       const int d0 = kSelBins - 1 - 2 * threadIdx.x;
-      const uint32_t h0 = hist[d0], h1 = hist[d0 - 1];
+      uint32_t h0 = 0, h1 = 0;
+#pragma unroll
+      for (int c = 0; c < kSelCopies; ++c) {
+        h0 += hist[c][d0];
+        h1 += hist[c][d0 - 1];
+        hist[c][d0] = hist[c][d0 - 1] = 0;
+      }
       uint32_t total;
       const uint32_t upto = block_scan(h0 + h1, ws, &total);
       const uint32_t above = upto - h0 - h1;
@@ -120,91 +149,156 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
     }
     ties = want;
   }
-  // Tokens in order, one per thread and pass; a pass reads before it writes, and
-  // writes only places up to those it read (mass_out may be mass).
-  uint32_t kept_before = 0, ties_before = 0;
-  for (int base = 0; base < len; base += kSelThreads) {
-    const int i = base + threadIdx.x;
-    float m = 0.f;
-    bool above = false, equal = false;
-    if (i < len) {
-      m = mass[i];
-      const uint32_t key = mass_key(m);
-      above = i >= cand || key > floor_key;
-      equal = i < cand && key == floor_key;
+  if constexpr (kKeep) {
+    // Every warp counts its run, learns what the runs before hold, and writes its kept tokens.
+    uint32_t n_above = 0, n_equal = 0;
+#pragma unroll 4
+    for (int i = begin + lane; i < end; i += 32) {
+      const uint32_t key = keys[i];
+      n_above += (i >= cand || key > floor_key) ? 1u : 0u;
+      n_equal += (i < cand && key == floor_key) ? 1u : 0u;
     }
-    uint32_t total;
-    const uint32_t scan = block_scan((above ? 1u << 16 : 0u) + (equal ? 1u : 0u), ws, &total);
-    // Ties before this token, and the tokens kept before it.
-    const uint32_t t_incl = ties_before + (scan & 0xffffu);
-    const uint32_t t_excl = t_incl - (equal ? 1u : 0u);
-    const bool keep = above || (equal && t_excl < ties);
-    const uint32_t slot = kept_before + (scan >> 16) - (above ? 1u : 0u) + min(t_excl, ties) - min(ties_before, ties);
-    if (keep) {
-      kept[slot] = i;
-      if (mass_out != nullptr) mass_out[slot] = m;
+    n_above = __reduce_add_sync(0xffffffffu, n_above);
+    n_equal = __reduce_add_sync(0xffffffffu, n_equal);
+    __syncthreads();
+    // (16 bits hold either count: 32768 tokens at most)
+    if (lane == 0) ws[warp] = n_above << 16 | (n_equal & 0xffffu);
+    __syncthreads();
+    uint32_t a = 0, e = 0;
+    for (int w = 0; w < warp; ++w) {
+      a += ws[w] >> 16;
+      e += ws[w] & 0xffffu;
     }
-    kept_before += (total >> 16) + min(ties_before + (total & 0xffffu), ties) - min(ties_before, ties);
-    ties_before += total & 0xffffu;
+    const uint32_t before_me = (1u << lane) - 1u;
+#pragma unroll 2
+    for (int i0 = begin; i0 < end; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t key = i < end ? keys[i] : 0u;
+      const bool above = i < end && (i >= cand || key > floor_key);
+      const bool equal = i < end && i < cand && key == floor_key;
+      const uint32_t ab = __ballot_sync(0xffffffffu, above), eb = __ballot_sync(0xffffffffu, equal);
+      const uint32_t my_a = a + __popc(ab & before_me), my_e = e + __popc(eb & before_me);
+      if (above || (equal && my_e < ties)) {
+        const uint32_t slot = my_a + min(my_e, ties);
+        kept[slot] = i;
+        if (mass_out != nullptr) mass_out[slot] = key_mass(key);
+      }
+      a += __popc(ab);
+      e += __popc(eb);
+    }
+  } else {
+    // Tokens in order, one per thread and pass; a pass reads before it writes, and
+    // writes only places up to those it read (mass_out may be mass).
+    uint32_t kept_before = 0, ties_before = 0;
+    for (int base = 0; base < len; base += kSelThreads) {
+      const int i = base + threadIdx.x;
+      float m = 0.f;
+      bool above = false, equal = false;
+      if (i < len) {
+        m = mass[i];
+        const uint32_t key = mass_key(m);
+        above = i >= cand || key > floor_key;
+        equal = i < cand && key == floor_key;
+      }
+      uint32_t total;
+      const uint32_t scan = block_scan((above ? 1u << 16 : 0u) + (equal ? 1u : 0u), ws, &total);
+      // Ties before this token, and the tokens kept before it.
+      const uint32_t t_excl = ties_before + (scan & 0xffffu) - (equal ? 1u : 0u);
+      if (above || (equal && t_excl < ties)) {
+        const uint32_t slot =
+            kept_before + (scan >> 16) - (above ? 1u : 0u) + min(t_excl, ties) - min(ties_before, ties);
+        kept[slot] = i;
+        if (mass_out != nullptr) mass_out[slot] = m;
+      }
+      kept_before += (total >> 16) + min(ties_before + (total & 0xffffu), ties) - min(ties_before, ties);
+      ties_before += total & 0xffffu;
+    }
   }
-  __syncthreads();
   for (int i = n_new + threadIdx.x; i < p.budget; i += kSelThreads) kept[i] = -1;
-  if (mass_out != nullptr) {
-    for (int i = n_new + threadIdx.x; i < most; i += kSelThreads) mass_out[i] = 0.f;
-  }
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveSlice = 4;  // 16-byte vectors of a row that one block moves
-constexpr int kMoveBatch = 4;  // of them per thread and pass
+constexpr int kMoveCluster = 8;          // blocks that move one head's K or V
+constexpr int kMoveBytes = 64 * 1024;    // rows a block reads before it writes them, in shared memory
 
-__global__ void __launch_bounds__(kMoveThreads) paged_evict_move_kernel(const EvictParams p) {
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n"
+      "barrier.cluster.wait.acquire.aligned;\n" ::
+          : "memory");
+}
+
+template <int D>
+__global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThreads)
+    paged_evict_move_kernel(const EvictParams p) {
+  constexpr int kVecs = D / 8;                   // 16-byte vectors of a row
+  constexpr int kRows = kMoveBytes / (D * 2);    // rows of a block's batch
+  constexpr int kItems = kMoveBytes / 16 / kMoveThreads;
+  extern __shared__ uint4 staged[];
+  __shared__ int2 rows[2][kRows];                // old and new token row in the cache, or -1
   grid_launch_dependents();
   grid_dependency_wait();
-  const int slices = p.s.D / (8 * kMoveSlice);
-  int u = blockIdx.x;
-  const int slice = u % slices;
-  u /= slices;
+  const int rank = blockIdx.x % kMoveCluster;
+  int u = blockIdx.x / kMoveCluster;
   const int kind = u % 2;
   u /= 2;
   const int h = u % p.s.Hkv, b = u / p.s.Hkv;
   const int most = p.s.max_pages * p.s.page_size;
   const int n_new = min(min(max(p.s.lengths[b], 0), most), p.budget);
-  if (h == 0 && kind == 0 && slice == 0 && threadIdx.x == 0) p.new_lengths[b] = n_new;
-  const int* kept = p.kept + (static_cast<size_t>(b) * p.s.Hkv + h) * p.budget;
+  if (h == 0 && kind == 0 && rank == 0 && threadIdx.x == 0) p.new_lengths[b] = n_new;
+  const size_t head = static_cast<size_t>(b) * p.s.Hkv + h;
+  const int* kept = p.kept + head * p.budget;
   const int* table = p.s.block_table + static_cast<size_t>(b) * p.s.max_pages;
   const int log2T = 31 - __clz(p.s.page_size);
   uint4* cache = static_cast<uint4*>(p.cache);
-  // The slice's vector of token position t, or -1 on a page out of range.
-  auto place = [&](int t) -> long long {
-    const int page = table[t >> log2T];
-    if (page < 0 || page >= p.s.num_pages) {
-      atomicExch(p.s.status, p.s.bad_index_code);
-      return -1;
+  // Where the rows of the batch at d0 come from and go to.
+  auto look_up = [&](int d0, int2* out) {
+    for (int r = threadIdx.x; r < kRows; r += kMoveThreads) {
+      const int d = d0 + rank * kRows + r;
+      int2 move = make_int2(-1, -1);
+      const int from = d < n_new ? kept[d] : d;
+      if (from != d) {
+        const int page_from = table[from >> log2T], page_to = table[d >> log2T];
+        if (page_from < 0 || page_from >= p.s.num_pages || page_to < 0 || page_to >= p.s.num_pages) {
+          atomicExch(p.s.status, p.s.bad_index_code);
+        } else {
+          const int in = p.s.page_size - 1;
+          move = make_int2(((page_from * 2 + kind) << log2T) + (from & in), ((page_to * 2 + kind) << log2T) + (d & in));
+        }
+      }
+      out[r] = move;
     }
-    const size_t row = (static_cast<size_t>(page) * 2 + kind) * p.s.page_size + (t & (p.s.page_size - 1));
-    return static_cast<long long>((row * p.s.Hkv + h) * (p.s.D / 8) + slice * kMoveSlice + threadIdx.x % kMoveSlice);
   };
-  constexpr int kRows = kMoveThreads / kMoveSlice;
-  for (int d0 = 0; d0 < n_new; d0 += kRows * kMoveBatch) {
-    uint4 v[kMoveBatch];
-    long long to[kMoveBatch];
+  auto place = [&](int row, int vec) -> size_t { return (static_cast<size_t>(row) * p.s.Hkv + h) * kVecs + vec; };
+  look_up(0, rows[0]);
+  __syncthreads();
+  int buf = 0;
+  for (int d0 = 0; d0 < n_new; d0 += kRows * kMoveCluster, buf ^= 1) {
 #pragma unroll
-    for (int i = 0; i < kMoveBatch; ++i) {
-      const int d = d0 + i * kRows + threadIdx.x / kMoveSlice;
-      to[i] = -1;
-      if (d >= n_new) continue;
-      const int from = kept[d];
-      if (from == d) continue;
-      const long long src = place(from);
-      to[i] = src < 0 ? -1 : place(d);
-      if (to[i] >= 0) v[i] = cache[src];
+    for (int i = 0; i < kItems; ++i) {
+      const int x = i * kMoveThreads + threadIdx.x;
+      const int from = rows[buf][x / kVecs].x;
+      if (from >= 0) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(staged + x)),
+                     "l"(cache + place(from, x % kVecs))
+                     : "memory");
+      }
     }
-    __syncthreads();  // the batch is read: its rows, and any behind them, may be overwritten
+    // The next batch's places are looked up while this one's rows are on their way.
+    look_up(d0 + kRows * kMoveCluster, rows[buf ^ 1]);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    cluster_barrier();  // the batch is read: its rows, and any behind them, may be overwritten
 #pragma unroll
-    for (int i = 0; i < kMoveBatch; ++i) {
-      if (to[i] >= 0) cache[to[i]] = v[i];
+    for (int i = 0; i < kItems; ++i) {
+      const int x = i * kMoveThreads + threadIdx.x;
+      const int to = rows[buf][x / kVecs].y;
+      if (to >= 0) cache[place(to, x % kVecs)] = staged[x];
     }
+    __syncthreads();  // rows[buf] is written again in the next round
+  }
+  if (kind == 0 && p.mass_out != nullptr) {  // no token is left there
+    float* mass_out = p.mass_out + head * most;
+    for (int i = n_new + rank * kMoveThreads + threadIdx.x; i < most; i += kMoveThreads * kMoveCluster) mass_out[i] = 0.f;
   }
 }
 

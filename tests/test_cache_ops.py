@@ -153,6 +153,9 @@ EVICT = {
     "ties_at_the_border": (2, 128, 16, [300, 150], "bf16", 101, 3, "few_values"),
     "odd_values": (2, 64, 16, [400], "fp16", 200, 0, "odd"),
     "long": (2, 128, 64, [9000, 5000], "fp16", 2049, 100, "spread"),
+    "past_shared_memory": (1, 64, 64, [40000, 33000], "fp16", 5000, 64, "spread"),
+    "past_shared_memory_ties": (2, 64, 64, [36000], "bf16", 20000, 5, "few_values"),
+    "most_stays": (2, 64, 16, [3000], "fp16", 2990, 100, "few_values"),
     "just_over": (4, 64, 16, [1025, 1024], "bf16", 1024, 1, "spread"),
 }
 
