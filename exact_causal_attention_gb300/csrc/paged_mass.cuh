@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
   };
   // Whole units: a place past a unit's middle cuts behind it.
   auto locate = [&](long long x) -> Place {
-    const LinePlace at = line_locate<true>(line, B, p.s.Hkv, x, cost);
+    const LinePlace at = line_locate<true>(line, B, p.s.Hkv, W, x, cost);
     Place r{at.b, at.item, at.head + (2 * at.in >= at.cost ? 1 : 0)};
     if (r.head == p.s.Hkv) {  // (the pair may then be one past the request's last)
       r.head = 0;

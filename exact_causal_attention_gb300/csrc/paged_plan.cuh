@@ -131,7 +131,11 @@ __device__ __forceinline__ long long line_build_warp(const LineTables& t, const 
     if (b >= d) upto += up;
   }
   long long sum = 0;
-  for (int r = 0; r < B; ++r) {
+  const int longest = __reduce_max_sync(0xffffffffu, mine);
+  if (longest <= 8) {  // every lane its own request's
+    for (int i = 0; i < longest; ++i) sum += i < mine ? cost(req, i) : 0;
+  }
+  for (int r = 0; longest > 8 && r < B; ++r) {
     const int4 q = make_int4(__shfl_sync(0xffffffffu, req.x, r), __shfl_sync(0xffffffffu, req.y, r),
                              __shfl_sync(0xffffffffu, req.z, r), __shfl_sync(0xffffffffu, req.w, r));
     const int n = __shfl_sync(0xffffffffu, mine, r);
@@ -183,57 +187,72 @@ struct LinePlace {
 
 // Called by a whole warp; x below the line's length.  kHeadsInside: a request's items
 // in order, each with all its heads; else its heads in order, each with all items.
-template <bool kHeadsInside, typename Cost>
-__device__ __forceinline__ LinePlace line_locate(const LineTables& t, int B, int heads, long long x, Cost cost) {
+// Int: a type that holds the line's length (64-bit arithmetic takes several times longer).
+template <bool kHeadsInside, typename Int, typename Cost>
+__device__ __forceinline__ LinePlace line_locate_as(const LineTables& t, int B, int heads, Int x, Cost cost) {
   const int lane = threadIdx.x % 32;
   LinePlace r;
   // Requests without items share their base with the next: the last such one has items.
-  r.b = last_at_most(t.base, B, x);
-  const long long sum = static_cast<long long>(t.cost[r.b]);
-  const long long in = x - t.base[r.b];
-  long long rest = in;
-  if constexpr (!kHeadsInside) {
-    r.head = ((in | sum) >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(sum))
-                                     : static_cast<int>(in / sum);
-    rest = in - r.head * sum;
+  if (B <= 32) {
+    r.b = __popc(__ballot_sync(0xffffffffu, lane < B && static_cast<Int>(t.base[min(lane, B - 1)]) <= x)) - 1;
+  } else {
+    r.b = last_at_most(t.base, B, static_cast<long long>(x));
   }
-  r.start = x - rest;
+  const Int sum = static_cast<Int>(t.cost[r.b]);
+  Int rest = x - static_cast<Int>(t.base[r.b]);
+  Int start = static_cast<Int>(t.base[r.b]);
+  r.head = 0;
+  if constexpr (!kHeadsInside) {
+    r.head = static_cast<int>(rest / sum);
+    start += static_cast<Int>(r.head) * sum;
+    rest -= static_cast<Int>(r.head) * sum;
+  }
   const int4 q = t.req[r.b];
   const int n = t.first[r.b + 1] - t.first[r.b];
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int i = i0 + lane;
     const int one = i < n ? cost(q, i) : 0;
-    const long long mine = kHeadsInside ? static_cast<long long>(one) * heads : one;
-    long long c = mine;
+    const Int mine = kHeadsInside ? static_cast<Int>(one) * heads : one;
+    Int c = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-      const long long up = __shfl_up_sync(0xffffffffu, c, d);
+      const Int up = __shfl_up_sync(0xffffffffu, c, d);
       if (lane >= d) c += up;
     }
     const unsigned here = __ballot_sync(0xffffffffu, i < n && rest < c);
     if (here != 0) {
       const int src = __ffs(here) - 1;
-      const long long before = __shfl_sync(0xffffffffu, c - mine, src);
+      const Int before = __shfl_sync(0xffffffffu, c - mine, src);
       r.item = i0 + src;
       r.cost = __shfl_sync(0xffffffffu, one, src);
-      long long at = rest - before;
-      r.start += before;
+      Int at = rest - before;
+      start += before;
       if constexpr (kHeadsInside) {
         r.head = static_cast<int>(at / r.cost);
-        at -= static_cast<long long>(r.head) * r.cost;
-        r.start += static_cast<long long>(r.head) * r.cost;
+        at -= static_cast<Int>(r.head) * r.cost;
+        start += static_cast<Int>(r.head) * r.cost;
       }
       r.in = static_cast<int>(at);
+      r.start = static_cast<long long>(start);
       return r;
     }
-    const long long all = __shfl_sync(0xffffffffu, c, 31);
+    const Int all = __shfl_sync(0xffffffffu, c, 31);
     rest -= all;
-    r.start += all;
+    start += all;
   }
   r.item = n;  // not reached: a request's items cover its stretch
-  r.head = 0;
   r.cost = r.in = 0;
+  r.start = static_cast<long long>(start);
   return r;
+}
+
+template <bool kHeadsInside, typename Cost>
+__device__ __forceinline__ LinePlace line_locate(const LineTables& t, int B, int heads, long long length, long long x,
+                                                 Cost cost) {
+  if (length < (1ll << 31)) {
+    return line_locate_as<kHeadsInside, uint32_t>(t, B, heads, static_cast<uint32_t>(x), cost);
+  }
+  return line_locate_as<kHeadsInside, unsigned long long>(t, B, heads, static_cast<unsigned long long>(x), cost);
 }
 
 }  // namespace eca

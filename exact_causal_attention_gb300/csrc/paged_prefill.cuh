@@ -42,7 +42,7 @@ constexpr int kPfTile = 128;          // keys per tile, and rows per query tile
 // What starting and ending a unit costs, in key tiles, and the least work a part of
 // the line is cut to.
 constexpr int kPfUnitCost = 3;
-constexpr int kPfMinCost = 4;
+constexpr int kPfMinCost = 3;
 constexpr int kPfMinPart = 2;         // a unit is not cut within so many tiles of its ends
 constexpr int kPfQueue = 4;
 constexpr int kPfReaders = 11;
@@ -133,10 +133,14 @@ __device__ __forceinline__ PairTiles pair_tiles(const PrefillParams& p, int n, i
   return u;
 }
 
-// Where a place y on a unit's own line (its cost is k + kPfUnitCost) cuts it: before
-// key tile 0 .. k.
+// Where a place y on a unit's own line (its cost is k + kPfUnitCost, shared by its tiles)
+// cuts it: before key tile 0 .. k.
 __device__ __forceinline__ int cut_tile(long long y, int k) {
-  const long long t = y - kPfUnitCost;
+  const long long cost = k + kPfUnitCost;
+  const long long t = y < (1 << 15) && k < (1 << 15)
+                          ? static_cast<long long>((static_cast<uint32_t>(y) * static_cast<uint32_t>(k) +
+                                                    static_cast<uint32_t>(cost) / 2) / static_cast<uint32_t>(cost))
+                          : (y * k + cost / 2) / cost;
   if (t < kPfMinPart) return 0;
   if (t > k - kPfMinPart) return k;
   return static_cast<int>(t);
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     long long start;  // of the unit, on the line
   };
   auto locate = [&](long long x) -> Place {
-    const LinePlace at = line_locate<false>(line, B, heads, x, cost);
+    const LinePlace at = line_locate<false>(line, B, heads, W, x, cost);
     const int k = at.cost - kPfUnitCost;
     return Place{at.b, at.head, at.item, cut_tile(at.in, k), k, at.start};
   };
@@ -252,6 +256,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       to.b = B;
     }
   }
+  // The first request's sizes, before the ring's copies overwrite the tables.
+  int4 first_req = make_int4(0, 0, 0, 0);
+  if (warp == 8 && has_work) first_req = line.req[from.b];
   // The plan's reads and writes come before the ring's copies (which this warp issues).
   fence_proxy_async_smem();
   if (!p.small_plan) {
@@ -325,7 +332,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       };
       while (ok && has_work && b <= end_b && b < B) {
         if (loaded != b) {
-          r = load_request(p.s, &p.f, b);
+          if (loaded < 0) {
+            r = Request{p.s.q_offsets[b], first_req.x, first_req.w, first_req.y, first_req.z};
+          } else {
+            r = load_request(p.s, &p.f, b);
+          }
           loaded = b;
         }
         const bool last = b == end_b && head == to.head && pair == to.pair;  // the unit the part ends in
@@ -352,23 +363,25 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           w.gap = u.gap;
           w.kv = tile;
           w.part = tile > 0 ? 2 * cta : (stop < u.k ? 2 * cta + 1 : -1);
+          auto first_page = [&](int j) -> int {  // of the j-th tile
+            const int v = tile + w.n_max - 1 - j;
+            return (v < u.pre ? v : v + u.gap) * pages;
+          };
+          // The first page ids are on their way while the fragment is handed out.
+          walk.from0 = u.w0;
+          walk.to0 = u.hi;
+          walk.prefix = r.prefix;
+          if (w.n_max > 0) {
+            walk.start(p.s.block_table + static_cast<size_t>(b) * p.s.max_pages, first_page(0) >> 5);
+          }
           if (!push(w)) {
             ok = false;
             break;
           }
           // K and V tiles of the fragment, alternating.
           const int kvh = head / p.chunks;
-          const int* table = p.s.block_table + static_cast<size_t>(b) * p.s.max_pages;
           // K/V that several units read stays in L2; a lone pair's is read once.
           const uint64_t pol = r.n > per_pair ? policy_evict_last() : policy_evict_first();
-          auto first_page = [&](int j) -> int {  // of the j-th tile
-            const int v = tile + w.n_max - 1 - j;
-            return (v < u.pre ? v : v + u.gap) * pages;
-          };
-          walk.from0 = u.w0;
-          walk.to0 = u.hi;
-          walk.prefix = r.prefix;
-          if (w.n_max > 0) walk.start(table, first_page(0) >> 5);
           for (int j = 0; ok && j < w.n_max; ++j) {
             const int at = walk.hold(first_page(j), p.s.status, p.s.bad_index_code);
             for (int kind = 0; kind < 2; ++kind) {
@@ -839,9 +852,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             tmem_wait_ld_x32(o);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              dst[static_cast<size_t>(c0 / 4 + i) * 256] =
-                  make_float4(__uint_as_float(o[4 * i]) * inv_l, __uint_as_float(o[4 * i + 1]) * inv_l,
-                              __uint_as_float(o[4 * i + 2]) * inv_l, __uint_as_float(o[4 * i + 3]) * inv_l);
+              if (row_ok) {
+                dst[static_cast<size_t>(c0 / 4 + i) * 256] =
+                    make_float4(__uint_as_float(o[4 * i]) * inv_l, __uint_as_float(o[4 * i + 1]) * inv_l,
+                                __uint_as_float(o[4 * i + 2]) * inv_l, __uint_as_float(o[4 * i + 3]) * inv_l);
+              }
             }
           }
         }
@@ -935,25 +950,43 @@ __global__ void __launch_bounds__(2 * D) paged_prefill_combine(const PrefillPara
   if (tok >= p.tq || tile * p.tq + tok >= split[2]) return;
   // CTA c left its part in its second slot, the following ones in their first.
   auto slot = [&](int i) -> size_t { return i == 0 ? 2 * cta + 1 : 2 * (cta + i); };
+  // Three parts' sums and outputs at a time in one round trip, folded in with the online law.
   float top = -INFINITY;
-  for (int i = 0; i < parts; ++i) top = fmaxf(top, p.part_lse[slot(i) * 256 + t]);
   float sum = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (top > -INFINITY) {
-    for (int i = 0; i < parts; ++i) {
-      const float w = exp2f(p.part_lse[slot(i) * 256 + t] - top);
+  for (int i0 = 0; i0 < parts; i0 += 3) {
+    float ls[3];
+    float4 x[3][4];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      ls[i] = -INFINITY;
+      if (i0 + i < parts) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot(i0 + i) * (D / 4) + c16 * 4) * 256 + t;
+        ls[i] = p.part_lse[slot(i0 + i) * 256 + t];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[i][v] = src[v * 256];
+      }
+    }
+    const float now = fmaxf(fmaxf(top, ls[0]), fmaxf(ls[1], ls[2]));
+    if (now == -INFINITY) continue;
+    const float keep = top == -INFINITY ? 0.f : exp2f(top - now);
+    top = now;
+    sum *= keep;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] = make_float4(acc[v].x * keep, acc[v].y * keep, acc[v].z * keep, acc[v].w * keep);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const float w = exp2f(ls[i] - now);
       if (w == 0.f) continue;  // (a part without keys for this row has written no output)
       sum += w;
-      const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot(i) * (D / 4) + c16 * 4) * 256 + t;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const float4 x = src[v * 256];
-        acc[v].x += w * x.x;
-        acc[v].y += w * x.y;
-        acc[v].z += w * x.z;
-        acc[v].w += w * x.w;
+        acc[v].x += w * x[i][v].x;
+        acc[v].y += w * x[i][v].y;
+        acc[v].z += w * x[i][v].z;
+        acc[v].w += w * x[i][v].w;
       }
     }
   }
