@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
       const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0);
       const uint32_t digits = round == 2 ? 0x3ffu : 0x7ffu;
       const int stop = min(end, cand);
-#pragma unroll 4
+#pragma unroll 8
       for (int i = begin + lane; i < stop; i += 32) {
         const uint32_t key = key_at(i);
         if ((key & mask) == floor_key) atomicAdd(&hist[lane % kSelCopies][(key >> shift) & digits], 1u);
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
   if constexpr (kKeep) {
     // Every warp counts its run, learns what the runs before hold, and writes its kept tokens.
     uint32_t n_above = 0, n_equal = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = begin + lane; i < end; i += 32) {
       const uint32_t key = keys[i];
       n_above += (i >= cand || key > floor_key) ? 1u : 0u;
@@ -170,21 +170,28 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
       e += ws[w] & 0xffffu;
     }
     const uint32_t before_me = (1u << lane) - 1u;
-#pragma unroll 2
-    for (int i0 = begin; i0 < end; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t key = i < end ? keys[i] : 0u;
-      const bool above = i < end && (i >= cand || key > floor_key);
-      const bool equal = i < end && i < cand && key == floor_key;
-      const uint32_t ab = __ballot_sync(0xffffffffu, above), eb = __ballot_sync(0xffffffffu, equal);
-      const uint32_t my_a = a + __popc(ab & before_me), my_e = e + __popc(eb & before_me);
-      if (above || (equal && my_e < ties)) {
-        const uint32_t slot = my_a + min(my_e, ties);
-        kept[slot] = i;
-        if (mass_out != nullptr) mass_out[slot] = key_mass(key);
+    constexpr int kGroups = 4;  // of 32 tokens at a time, so that their votes overlap
+    for (int i0 = begin; i0 < end; i0 += 32 * kGroups) {
+      uint32_t key[kGroups], ab[kGroups], eb[kGroups];
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int i = i0 + 32 * g + lane;
+        key[g] = i < end ? keys[i] : 0u;
+        ab[g] = __ballot_sync(0xffffffffu, i < end && (i >= cand || key[g] > floor_key));
+        eb[g] = __ballot_sync(0xffffffffu, i < end && i < cand && key[g] == floor_key);
       }
-      a += __popc(ab);
-      e += __popc(eb);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const uint32_t my_a = a + __popc(ab[g] & before_me), my_e = e + __popc(eb[g] & before_me);
+        const bool above = (ab[g] >> lane) & 1u, equal = (eb[g] >> lane) & 1u;
+        if (above || (equal && my_e < ties)) {
+          const uint32_t slot = my_a + min(my_e, ties);
+          kept[slot] = i0 + 32 * g + lane;
+          if (mass_out != nullptr) mass_out[slot] = key_mass(key[g]);
+        }
+        a += __popc(ab[g]);
+        e += __popc(eb[g]);
+      }
     }
   } else {
     // Tokens in order, one per thread and pass; a pass reads before it writes, and

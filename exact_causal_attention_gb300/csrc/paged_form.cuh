@@ -3,8 +3,9 @@
 // cap tanh(scale x / cap) takes one exponential and one reciprocal as 1 - 2 / (1 + e^2y), which
 // would treble the work of the unit that the softmax's own exponential needs.  Scores are
 // mostly well inside the cap, where tanh(y) = y P(y^2) takes multiply-adds alone: P is a
-// polynomial of degree 7 fitted to tanh(y) / y on |y| <= 1.25 by iteratively reweighted least squares
-// (relative error 8e-8 before rounding).  A group of scores with one outside takes the other way.
+// polynomial fitted to tanh(y) / y by iteratively reweighted least squares, of degree 5 on
+// |y| <= 0.75 or 7 on |y| <= 1.25 (relative errors 3e-8 and 8e-8 before rounding).  A group of scores
+// with one outside takes the exponential.
 #pragma once
 #include "paged_common.cuh"
 
@@ -19,22 +20,26 @@ constexpr int kFormCap = 2;   // tanh cap, with or without a bias
 struct CapScale {
   float in;     // scale / cap
   float out;    // cap unit
-  float limit;  // |x| up to which the polynomial holds
-  float2 c[8];  // its coefficients for x^2, with the scales folded in, for pairs of scores
+  float near, far;  // |x| up to which the shorter and the longer polynomial hold
+  // Their coefficients for x^2, with the scales folded in, for pairs of scores.
+  float2 n[6], f[8];
 };
 
 __device__ __forceinline__ CapScale cap_scale(float scale, float softcap, float unit) {
-  constexpr float kRange = 1.25f;
-  constexpr float kCoef[8] = {0.99999994f,    -0.333327f,     0.13324507f,    -0.05349034f,
-                              0.020557173f, -0.0067961547f, 0.0015881141f, -0.00018259805f};
+  constexpr float kNear = 0.75f, kFar = 1.25f;
+  constexpr float kNearCoef[6] = {1.0f, -0.333329588f, 0.133254066f, -0.0533444285f, 0.0195829086f, -0.0047162571f};
+  constexpr float kFarCoef[8] = {0.99999994f,    -0.333327f,     0.13324507f,    -0.05349034f,
+                                 0.020557173f, -0.0067961547f, 0.0015881141f, -0.00018259805f};
   CapScale r;
   r.in = softcap > 0.f ? scale / softcap : 0.f;
   r.out = softcap * unit;
-  r.limit = r.in > 0.f ? kRange / r.in : 0.f;
-  float f = r.out * r.in;
+  r.near = r.in > 0.f ? kNear / r.in : 0.f;
+  r.far = r.in > 0.f ? kFar / r.in : 0.f;
+  float f = scale * unit;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    r.c[i] = make_float2(kCoef[i] * f, kCoef[i] * f);
+    if (i < 6) r.n[i] = make_float2(kNearCoef[i] * f, kNearCoef[i] * f);
+    r.f[i] = make_float2(kFarCoef[i] * f, kFarCoef[i] * f);
     f *= r.in * r.in;
   }
   return r;
@@ -47,26 +52,41 @@ __device__ __forceinline__ float tanh_wide(float y) {
   return fmaf(-2.f, r, 1.f);
 }
 
-// A whole warp: 32 scores per thread, x to unit cap tanh(x scale / cap).
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k) {
+// A whole warp: 32 scores per thread, x to unit cap tanh(x scale / cap), plus add[i] where
+// there is one (in shared memory, 16-byte aligned, the same for every thread).
+template <bool kAdd>
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k, const float* add) {
   float mx = 0.f;
 #pragma unroll
   for (int i = 0; i < 32; i += 2) mx = fmax3(mx, fabsf(__uint_as_float(s[i])), fabsf(__uint_as_float(s[i + 1])));
-  if (__all_sync(0xffffffffu, mx <= k.limit)) {
+  auto polynomial = [&](const auto& c) {
+    constexpr int kTerms = sizeof(c) / sizeof(float2);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const float2 x = make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
       const float2 z = __fmul2_rn(x, x);
-      float2 a = k.c[7];
+      float2 a = c[kTerms - 1];
 #pragma unroll
-      for (int j = 6; j >= 0; --j) a = __ffma2_rn(a, z, k.c[j]);
-      a = __fmul2_rn(a, x);
+      for (int j = kTerms - 2; j >= 0; --j) a = __ffma2_rn(a, z, c[j]);
+      if constexpr (kAdd) {
+        a = __ffma2_rn(a, x, *reinterpret_cast<const float2*>(add + i));
+      } else {
+        a = __fmul2_rn(a, x);
+      }
       s[i] = __float_as_uint(a.x);
       s[i + 1] = __float_as_uint(a.y);
     }
+  };
+  if (__all_sync(0xffffffffu, mx <= k.near)) {
+    polynomial(k.n);
+  } else if (__all_sync(0xffffffffu, mx <= k.far)) {
+    polynomial(k.f);
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(k.out * tanh_wide(__uint_as_float(s[i]) * k.in));
+    for (int i = 0; i < 32; ++i) {
+      const float t = tanh_wide(__uint_as_float(s[i]) * k.in);
+      s[i] = __float_as_uint(kAdd ? fmaf(k.out, t, add[i]) : k.out * t);
+    }
   }
 }
 

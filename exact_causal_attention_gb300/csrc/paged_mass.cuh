@@ -15,7 +15,8 @@
 // double-buffered per slot and read whole into registers, so the next product never waits for the sums.
 //
 // e^(s - lse) is taken as 2^(log2e (s - lse)) with the difference formed first in natural units: where
-// the weight matters s is near lse, so the one rounding of the difference is small.
+// the weight matters s is near lse, so the one rounding of the difference is small.  (With a cap both are
+// in base 2 from the start: its own error is larger, and the difference then costs nothing.)
 #pragma once
 #include <cuda.h>
 
@@ -408,6 +409,8 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     }
   } else if (warp == 11) {
     // ------------------------------------------------- the columns' values, lane by column
+    // (in base 2 with a cap, whose scores come in base 2)
+    const float lse_unit = FORM == kFormCap ? kLog2e : 1.f;
     int tok[4], head[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
           next[c] = -INFINITY;
           if (tok[c] < p.tq && t0 + tok[c] < w.n) {
             const float z = p.lse[static_cast<size_t>(w.row0 + t0 + tok[c]) * p.Hq + (w.kvh * p.chunks + chunk) * p.hc + head[c]];
-            next[c] = z == -INFINITY ? z : -z;
+            next[c] = z == -INFINITY ? z : -z * lse_unit;
           }
         }
       };
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
         for (int c = 0; c < 4; ++c) {
           dst[lane + 32 * c] = now[c];
           if (FORM != kFormPlain && p.f.slopes != nullptr) {
-            dst[kMsCols + lane + 32 * c] = p.f.slopes[(w.kvh * p.chunks + chunk) * p.hc + head[c]];
+            dst[kMsCols + lane + 32 * c] = lse_unit * p.f.slopes[(w.kvh * p.chunks + chunk) * p.hc + head[c]];
             dst[2 * kMsCols + lane + 32 * c] = static_cast<float>(w.pos0 + t0 + tok[c]);
           }
         }
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     const uint32_t t_s = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + 256u * x;
     const int log2T = 31 - __clz(p.s.page_size);
     auto warp_wait = [&](uint32_t b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, wd.wait(b, ph)) != 0; };
-    const CapScale cap = cap_scale(p.f.scale, p.f.softcap, 1.f);
+    const CapScale cap = cap_scale(p.f.scale, p.f.softcap, kLog2e);
     int it = 0, step = 0, uses = 0;
     bool ok = true;
     MassUnit w;
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
         const int quarters = (cols + 31) / 32;
         // Sums 32 columns: 2^(log2e (form(s) - lse)).
         auto add = [&](uint32_t (&v)[32], int q) {
-          if constexpr (FORM == kFormCap) cap_scores(v, cap);
+          if constexpr (FORM == kFormCap) cap_scores<true>(v, cap, col + 32 * q);
           const float2 c2 = make_float2(p.f.scale, p.f.scale), k2 = make_float2(kLog2e, kLog2e);
           const bool biased = FORM == kFormBias || (FORM == kFormCap && p.f.slopes != nullptr);
           const bool all = __all_sync(0xffffffffu, lo <= 32 * q && hi >= 32 * q + 32) != 0;
@@ -537,13 +540,10 @@ __global__ void __launch_bounds__(kMsThreads, 1)
           const uint32_t seen = low(hi - 32 * q) & ~low(lo - 32 * q);
 #pragma unroll
           for (int i4 = 0; i4 < 32; i4 += 4) {
-            const float4 z = *reinterpret_cast<const float4*>(col + 32 * q + i4);  // - lse
             float2 y0 = make_float2(__uint_as_float(v[i4]), __uint_as_float(v[i4 + 1]));
             float2 y1 = make_float2(__uint_as_float(v[i4 + 2]), __uint_as_float(v[i4 + 3]));
-            if constexpr (FORM == kFormCap) {
-              y0 = __fadd2_rn(y0, make_float2(z.x, z.y));
-              y1 = __fadd2_rn(y1, make_float2(z.z, z.w));
-            } else {
+            if constexpr (FORM != kFormCap) {
+              const float4 z = *reinterpret_cast<const float4*>(col + 32 * q + i4);  // - lse
               y0 = __ffma2_rn(y0, c2, make_float2(z.x, z.y));
               y1 = __ffma2_rn(y1, c2, make_float2(z.z, z.w));
             }
@@ -555,8 +555,10 @@ __global__ void __launch_bounds__(kMsThreads, 1)
               y1.x = fmaf(-sl.z, fabsf(ps.z - key_f), y1.x);
               y1.y = fmaf(-sl.w, fabsf(ps.w - key_f), y1.y);
             }
-            y0 = __fmul2_rn(y0, k2);
-            y1 = __fmul2_rn(y1, k2);
+            if constexpr (FORM != kFormCap) {
+              y0 = __fmul2_rn(y0, k2);
+              y1 = __fmul2_rn(y1, k2);
+            }
             v[i4] = __float_as_uint(ex2(y0.x));
             v[i4 + 1] = __float_as_uint(ex2(y0.y));
             v[i4 + 2] = __float_as_uint(ex2(y1.x));

@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           uint32_t s[32];
           tmem_ld_x32(t_s + 32u * q, s);
           tmem_wait_ld_x32(s);
-          if constexpr (FORM == kFormCap) cap_scores(s, cap);
+          if constexpr (FORM == kFormCap) cap_scores<false>(s, cap, nullptr);
           if (FORM == kFormBias || (FORM == kFormCap && p.f.slopes != nullptr)) {
             const float away = static_cast<float>(pos - kb - 32 * q);
 #pragma unroll
