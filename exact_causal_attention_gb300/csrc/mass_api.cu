@@ -6,15 +6,22 @@ namespace {
 
 using namespace eca_host;
 
-template <int D, bool BF16, int FORM>
-int launch_mass(const CUtensorMap& tm_q, const CUtensorMap& tm_cache, const eca::MassParams& p, int grid,
+template <int D, bool BF16, int FORM, int kParts>
+int launch_mass_parts(const CUtensorMap& tm_q, const CUtensorMap& tm_cache, const eca::MassParams& p, int grid,
                 const Device& dev, cudaStream_t stream) {
   using L = eca::MassSmem<D>;
   static std::atomic<uint64_t> done{0};
-  const int rc = configure(eca::paged_mass_kernel<D, BF16, FORM>, dev, &done, L::kDynamicBytes, 0);
+  const int rc = configure(eca::paged_mass_kernel<D, BF16, FORM, kParts>, dev, &done, L::kDynamicBytes, 0);
   if (rc != ATTN_OK) return rc;
-  return launched(launch_pdl(eca::paged_mass_kernel<D, BF16, FORM>, static_cast<unsigned>(grid), eca::kMsThreads,
-                             L::kDynamicBytes, stream, tm_q, tm_cache, p));
+  return launched(launch_pdl(eca::paged_mass_kernel<D, BF16, FORM, kParts>, static_cast<unsigned>(grid),
+                             eca::kMsThreads<kParts>, L::kDynamicBytes, stream, tm_q, tm_cache, p));
+}
+
+template <int D, bool BF16, int FORM>
+int launch_mass(const CUtensorMap& tm_q, const CUtensorMap& tm_cache, const eca::MassParams& p, int grid,
+                const Device& dev, cudaStream_t stream) {
+  return p.hc * p.tq > 64 ? launch_mass_parts<D, BF16, FORM, 2>(tm_q, tm_cache, p, grid, dev, stream)
+                          : launch_mass_parts<D, BF16, FORM, 1>(tm_q, tm_cache, p, grid, dev, stream);
 }
 
 template <int D, bool BF16>

@@ -3,11 +3,12 @@
 // kept, and of the others the budget - recent with the largest mass (equal masses: the
 // lowest position first); the kept rows move in order to positions 0 .. budget - 1.
 //
-// Two kernels.  paged_evict_select: one block per (request, head) finds the mass of
-// the last token that is kept by a radix select on the masses' bit patterns (three
-// digits of 11, 11 and 10 bits; a histogram of the tokens that share the digits
-// fixed so far, in shared memory), then walks the tokens in order and gives every kept one its new
-// position.  The masses of up to 32K tokens are read once and kept in shared memory as keys.
+// Two kernels.  paged_evict_select: a cluster of 1 to 4 blocks per (request, head), each with a run of
+// its tokens, finds the mass of the last token that is kept by a radix select on the masses' bit
+// patterns (three digits of 11, 11 and 10 bits; a histogram of the tokens that share the digits
+// fixed so far, summed over the cluster through its shared memory), then walks the tokens in
+// order and gives every kept one its new position.  The masses are read once and kept in shared
+// memory as keys.  Bound by instructions (some 40 per token), so few heads are spread over more blocks.
 // paged_evict_move: the rows move in place.  A kept token's new position never exceeds its old
 // one and both grow together, so a batch of rows in order may be written once it has been
 // read, and never touches a row of a later batch.  A cluster of 8 blocks takes one head's K or V: they
@@ -66,44 +67,66 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* ws, uint32_
 }
 
 constexpr int kSelCopies = 4;          // of the histogram: lanes of a warp often meet in one bin
-constexpr int kSelSmemTokens = 32768;  // most tokens whose keys are kept in shared memory
+constexpr int kSelSmemTokens = 32768;  // most tokens of a block whose keys are kept in shared memory
+constexpr int kSelMaxCluster = 4;
 
-// kKeep: every request's keys fit in (dynamic) shared memory, 4 bytes a token.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n"
+      "barrier.cluster.wait.acquire.aligned;\n" ::
+          : "memory");
+}
+
+// A word of the shared memory of the cluster's block `rank`.
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, int rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// kKeep: every block's keys fit in (dynamic) shared memory, 4 bytes a token; otherwise
+// launched without a cluster, and the masses are read again for every digit.
 template <bool kKeep>
-__global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const EvictParams p, int cluster) {
   static_assert(kSelThreads == 1024, "block_scan reads one sum per warp of a full block");
   __shared__ uint32_t hist[kSelCopies][kSelBins];
+  __shared__ uint32_t merged[kKeep ? 3 : 1][kSelBins];  // this block's counts, one array per digit
   __shared__ uint32_t ws[32];
   __shared__ uint32_t chosen[2];  // digit, candidates above it
+  __shared__ uint32_t totals[2];  // this block's kept and tied tokens
   extern __shared__ uint32_t keys[];
   grid_launch_dependents();
   for (int i = threadIdx.x; i < kSelCopies * kSelBins; i += kSelThreads) (&hist[0][0])[i] = 0;
   grid_dependency_wait();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int b = blockIdx.x / p.s.Hkv;
+  const int rank = blockIdx.x % cluster, unit = blockIdx.x / cluster;  // unit: (b, head)
+  const int b = unit / p.s.Hkv;
   const int most = p.s.max_pages * p.s.page_size;
   int len = p.s.lengths[b];
   if (len < 0 || len > most) {
     if (threadIdx.x == 0) atomicExch(p.s.status, p.s.bad_index_code);
     len = len < 0 ? 0 : most;
   }
-  const float* mass = p.mass + static_cast<size_t>(blockIdx.x) * most;
-  float* mass_out = p.mass_out == nullptr ? nullptr : p.mass_out + static_cast<size_t>(blockIdx.x) * most;
-  int* kept = p.kept + static_cast<size_t>(blockIdx.x) * p.budget;
+  const float* mass = p.mass + static_cast<size_t>(unit) * most;
+  float* mass_out = p.mass_out == nullptr ? nullptr : p.mass_out + static_cast<size_t>(unit) * most;
+  int* kept = p.kept + static_cast<size_t>(unit) * p.budget;
   const int n_new = min(len, p.budget);
   const int tail = min(p.recent, n_new);
   const int cand = len - tail;        // tokens that compete: 0 .. cand - 1
   uint32_t want = n_new - tail;       // that many of them are kept
-  // Each warp takes a run of tokens.
-  const int run = ((len + 1023) / 1024) * 32;
-  const int begin = min(len, warp * run), end = min(len, begin + run);
+  // Each block takes a run of tokens, and each of its warps a run of those.
+  const int share = ((len + 32 * cluster - 1) / (32 * cluster)) * 32;
+  const int run = ((share + 1023) / 1024) * 32;
+  const int first = rank * share, past = min(len, first + share);
+  const int begin = min(past, first + warp * run), end = min(past, begin + run);
   __syncthreads();
   if constexpr (kKeep) {
 #pragma unroll 8
-    for (int i = begin + lane; i < end; i += 32) keys[i] = mass_key(mass[i]);
+    for (int i = begin + lane; i < end; i += 32) keys[i - first] = mass_key(mass[i]);
     __syncwarp();
   }
-  auto key_at = [&](int i) -> uint32_t { return kKeep ? keys[i] : mass_key(mass[i]); };
+  auto key_at = [&](int i) -> uint32_t { return kKeep ? keys[i - first] : mass_key(mass[i]); };
   // Keys above `floor_key` are kept, and the first `ties` of those equal to it.
   uint32_t floor_key = 0, ties = 0;
   if (want == static_cast<uint32_t>(cand)) {
@@ -131,6 +154,19 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
         h1 += hist[c][d0 - 1];
         hist[c][d0] = hist[c][d0 - 1] = 0;
       }
+      if (kKeep && cluster > 1) {
+        merged[kKeep ? round : 0][d0] = h0;
+        merged[kKeep ? round : 0][d0 - 1] = h1;
+        cluster_barrier();
+        h0 = h1 = 0;
+#pragma unroll
+        for (int c = 0; c < kSelMaxCluster; ++c) {
+          if (c < cluster) {
+            h0 += cluster_load(&merged[kKeep ? round : 0][d0], c);
+            h1 += cluster_load(&merged[kKeep ? round : 0][d0 - 1], c);
+          }
+        }
+      }
       uint32_t total;
       const uint32_t upto = block_scan(h0 + h1, ws, &total);
       const uint32_t above = upto - h0 - h1;
@@ -154,7 +190,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
     uint32_t n_above = 0, n_equal = 0;
 #pragma unroll 8
     for (int i = begin + lane; i < end; i += 32) {
-      const uint32_t key = keys[i];
+      const uint32_t key = keys[i - first];
       n_above += (i >= cand || key > floor_key) ? 1u : 0u;
       n_equal += (i < cand && key == floor_key) ? 1u : 0u;
     }
@@ -169,6 +205,17 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
       a += ws[w] >> 16;
       e += ws[w] & 0xffffu;
     }
+    if (cluster > 1) {
+      if (threadIdx.x == kSelThreads - 32) {
+        totals[0] = a + n_above;
+        totals[1] = e + n_equal;
+      }
+      cluster_barrier();
+      for (int c = 0; c < rank; ++c) {
+        a += cluster_load(&totals[0], c);
+        e += cluster_load(&totals[1], c);
+      }
+    }
     const uint32_t before_me = (1u << lane) - 1u;
     constexpr int kGroups = 4;  // of 32 tokens at a time, so that their votes overlap
     for (int i0 = begin; i0 < end; i0 += 32 * kGroups) {
@@ -176,7 +223,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const int i = i0 + 32 * g + lane;
-        key[g] = i < end ? keys[i] : 0u;
+        key[g] = i < end ? keys[i - first] : 0u;
         ab[g] = __ballot_sync(0xffffffffu, i < end && (i >= cand || key[g] > floor_key));
         eb[g] = __ballot_sync(0xffffffffu, i < end && i < cand && key[g] == floor_key);
       }
@@ -221,19 +268,13 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const E
       ties_before += total & 0xffffu;
     }
   }
-  for (int i = n_new + threadIdx.x; i < p.budget; i += kSelThreads) kept[i] = -1;
+  for (int i = n_new + rank * kSelThreads + threadIdx.x; i < p.budget; i += kSelThreads * cluster) kept[i] = -1;
+  if (kKeep && cluster > 1) cluster_barrier();  // no block leaves while another may read its counts
 }
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveCluster = 8;          // blocks that move one head's K or V
 constexpr int kMoveBytes = 64 * 1024;    // rows a block reads before it writes them, in shared memory
-
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile(
-      "barrier.cluster.arrive.release.aligned;\n"
-      "barrier.cluster.wait.acquire.aligned;\n" ::
-          : "memory");
-}
 
 template <int D>
 __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThreads)

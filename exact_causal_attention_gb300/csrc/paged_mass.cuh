@@ -10,9 +10,13 @@
 // A CTA takes an equal part of the line of units (paged_plan.cuh): two consecutive key tiles of one
 // (request, head), one per slot, with the heads of a pair of tiles side by side, as they lie in
 // memory (a token's heads are contiguous).  The queries' steps stream through a ring that both slots share.
-// 384 threads: warps 0-3 and 4-7 sum slots 0 and 1, warp 8 produces key tiles from their pages, warp 9
-// issues the MMAs, warp 10 loads Q, warp 11 the columns' log-sum-exps (and slopes and positions).  S^T is
-// double-buffered per slot and read whole into registers, so the next product never waits for the sums.
+// Warps: 4 per slot that sum (8 where a step has more than 64 columns: the first four then take
+// columns 0-63, the others 64-127), and four more: one produces key tiles from their pages, one issues
+// the MMAs, one loads Q, one the columns' log-sum-exps (and slopes and positions).  With 4 per slot the
+// sums wait for latencies, two warps per scheduler keeping the exponential unit at half its rate (500
+// tokens, 12000 keys: 102 us, with 8 warps 86); where a step has few columns more warps only take
+// issue slots from the producer (a decode step at 32K: 90 us, with 8 warps 100).  S^T is double-buffered
+// per slot, so the next product does not wait for the sums.
 //
 // e^(s - lse) is taken as 2^(log2e (s - lse)) with the difference formed first in natural units: where
 // the weight matters s is near lse, so the one rounding of the difference is small.  (With a cap both are
@@ -26,12 +30,12 @@
 
 namespace eca {
 
-constexpr int kMsThreads = 384;
+template <int kParts>
+constexpr int kMsThreads = 32 * (8 * kParts + 4);
 constexpr int kMsTile = 128;       // keys per tile
 constexpr int kMsCols = 128;       // most columns of a step
 constexpr int kMsPairCost = 2;     // a pair of key tiles' own cost, in steps
 constexpr int kMsQueue = 4;
-constexpr int kMsReaders = 11;
 constexpr int kMsColStages = 4;    // ring of the columns' values
 // Per key tile, which of its pages have a bad id.  The sums may trail the products by two steps
 // (four tiles), and the producer runs ahead of those by the ring.
@@ -75,13 +79,16 @@ struct MassSmem {
   static constexpr int kBarUnitFull = kBarSFree + 4;
   static constexpr int kBarUnitFree = kBarUnitFull + kMsQueue;
   static constexpr int kBarDrain = kBarUnitFree + kMsQueue;
-  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kBarSumFull = kBarDrain + 1;    // + 2 slot + unit parity: the second half's sums
+  static constexpr int kBarSumFree = kBarSumFull + 4;  // + 2 slot + unit parity
+  static constexpr int kNumBars = kBarSumFree + 4;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kBadOff = kMiscOff + 8;
   static constexpr int kQueueOff = (kBadOff + 4 * kMsBadRing + 15) & ~15;
   static constexpr int kEntryInts = 16;
   static constexpr int kScanOff = kQueueOff + kMsQueue * kEntryInts * 4;
-  static constexpr int kBytes = kScanOff + 16 * 8;
+  static constexpr int kSumOff = kScanOff + 24 * 8;  // fp32 [slot][unit parity][128]
+  static constexpr int kBytes = kSumOff + 4 * kMsTile * 4;
   static constexpr int kDynamicBytes = kBytes + 1024;
   static_assert(kLineTableBytes <= kColOff, "the plan's tables fit over the rings");
   static_assert(kDynamicBytes <= 227 * 1024, "shared memory exceeds the per-block limit");
@@ -113,11 +120,14 @@ struct MassUnit {
   int kvh, b;
 };
 
-template <int D, bool BF16, int FORM>
-__global__ void __launch_bounds__(kMsThreads, 1)
+// kParts: the warp groups that share a step's columns.
+template <int D, bool BF16, int FORM, int kParts>
+__global__ void __launch_bounds__(kMsThreads<kParts>, 1)
     paged_mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_cache,
                       const MassParams p) {
   using L = MassSmem<D>;
+  constexpr int kProducer = 8 * kParts, kIssuer = kProducer + 1, kQLoader = kProducer + 2, kColumns = kProducer + 3;
+  constexpr int kReaders = kProducer + 3;  // of a unit: every warp but the producer
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;
@@ -142,26 +152,28 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     }
     for (int s = 0; s < kMsColStages; ++s) {
       mbar_init(bar(L::kBarColFull + s), 1);
-      mbar_init(bar(L::kBarColEmpty + s), 8);
+      mbar_init(bar(L::kBarColEmpty + s), 8 * kParts);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(bar(L::kBarS + s), 1);
-      mbar_init(bar(L::kBarSFree + s), 4);
+      mbar_init(bar(L::kBarSFree + s), 4 * kParts);
+      mbar_init(bar(L::kBarSumFull + s), 4);
+      mbar_init(bar(L::kBarSumFree + s), 4);
     }
     for (int q = 0; q < kMsQueue; ++q) {
       mbar_init(bar(L::kBarUnitFull + q), 1);
-      mbar_init(bar(L::kBarUnitFree + q), kMsReaders);
+      mbar_init(bar(L::kBarUnitFree + q), kReaders);
     }
     mbar_init(bar(L::kBarDrain), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == kIssuer) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) tma_prefetch_map(&tm_cache);
-  if (warp == 10 && lane == 0) tma_prefetch_map(&tm_q);
+  if (warp == kProducer && lane == 0) tma_prefetch_map(&tm_cache);
+  if (warp == kQLoader && lane == 0) tma_prefetch_map(&tm_q);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -192,8 +204,8 @@ __global__ void __launch_bounds__(kMsThreads, 1)
   // Only the producer needs the plan; a long one is laid out by the whole block.
   long long W = 0;
   if (!p.small_plan) {
-    W = line_build<kMsThreads>(line, p.s, p.f, p.s.Hkv, items, cost);
-  } else if (warp == 8) {
+    W = line_build<kMsThreads<kParts>>(line, p.s, p.f, p.s.Hkv, items, cost);
+  } else if (warp == kProducer) {
     W = line_build_warp(line, p.s, p.f, p.s.Hkv, items, cost);
   }
   const int cta = static_cast<int>(blockIdx.x), G = static_cast<int>(gridDim.x);
@@ -211,7 +223,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     return r;
   };
   Place from = {B, 0, 0}, to = {B, 0, 0};
-  if (warp == 8 && W > 0) {
+  if (warp == kProducer && W > 0) {
     from = locate(line_cut(W, G, cta));
     if (cta + 1 < G) to = locate(line_cut(W, G, cta + 1));
   }
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     return true;
   };
 
-  if (warp == 8) {
+  if (warp == kProducer) {
     // ------------------------------------------------------------ key tiles, from pages
     const int T = p.s.page_size;
     const int log2T = 31 - __clz(T);
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     for (int x = (it > L::kKStages ? it - L::kKStages : 0); x < it; ++x) {
       wd.drain(bar(L::kBarKFull + x % L::kKStages), parity(x / L::kKStages));
     }
-  } else if (warp == 9) {
+  } else if (warp == kIssuer) {
     // ------------------------------------------------------------------ MMA issuer
     const uint64_t k_desc = TileLayout<D>::k_desc(sbase + L::kKOff);
     const uint64_t q_desc = smem_desc_sw128(sbase + L::kQOff, 16, 1024);
@@ -380,7 +392,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     }
     tc_commit_warp(bar(L::kBarDrain));
     wd.drain(bar(L::kBarDrain), 0);
-  } else if (warp == 10) {
+  } else if (warp == kQLoader) {
     // --------------------------------------------------------------------- Q loader
     if (lane == 0) {
       const uint64_t pol = policy_evict_last();  // every key tile of the request meets these rows
@@ -407,7 +419,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
         wd.drain(bar(L::kBarQFull + x % L::kQStages), parity(x / L::kQStages));
       }
     }
-  } else if (warp == 11) {
+  } else if (warp == kColumns) {
     // ------------------------------------------------- the columns' values, lane by column
     // (in base 2 with a cap, whose scores come in base 2)
     const float lse_unit = FORM == kFormCap ? kLog2e : 1.f;
@@ -462,13 +474,16 @@ __global__ void __launch_bounds__(kMsThreads, 1)
     }
   } else {
     // -------------------------------------------------------------------------- sums
-    const int x = warp / 4;  // slot
+    const int x = warp / (4 * kParts);     // slot
+    const int half = (warp / 4) % kParts;  // columns 64 half .. of every step
     const int r_local = (warp % 4) * 32 + lane;
     const uint32_t t_s = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + 256u * x;
     const int log2T = 31 - __clz(p.s.page_size);
     auto warp_wait = [&](uint32_t b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, wd.wait(b, ph)) != 0; };
     const CapScale cap = cap_scale(p.f.scale, p.f.softcap, kLog2e);
+    float* sums_s = reinterpret_cast<float*>(smem + L::kSumOff) + 2 * x * kMsTile;
     int it = 0, step = 0, uses = 0;
+    int joined = 0;  // units of this slot whose halves were joined
     bool ok = true;
     MassUnit w;
     while (ok) {
@@ -488,7 +503,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kBarColEmpty + cs));
         }
-        if (ok && !p.accumulate && key < most) {
+        if (ok && !p.accumulate && half == 0 && key < most) {
           p.mass[(static_cast<size_t>(w.b) * p.s.Hkv + w.kvh) * most + key] = 0.f;  // past the context
         }
         continue;
@@ -520,8 +535,6 @@ __global__ void __launch_bounds__(kMsThreads, 1)
         }
         ++uses;
         tc_fence_after_sync();
-        uint32_t s[2][32];
-        tmem_ld_x32(t_b, s[0]);
         if (i == 0) bad = bad_pages[item % kMsBadRing];
         const int cs = step % kMsColStages;
         if (!warp_wait(bar(L::kBarColFull + cs), parity(step / kMsColStages))) {
@@ -529,7 +542,6 @@ __global__ void __launch_bounds__(kMsThreads, 1)
           break;
         }
         const float* col = cols_s + cs * 3 * kMsCols;
-        const int quarters = (cols + 31) / 32;
         // Sums 32 columns: 2^(log2e (form(s) - lse)).
         auto add = [&](uint32_t (&v)[32], int q) {
           if constexpr (FORM == kFormCap) cap_scores<true>(v, cap, col + 32 * q);
@@ -575,35 +587,47 @@ __global__ void __launch_bounds__(kMsThreads, 1)
             acc[(e / 2) % 4] = __fadd2_rn(acc[(e / 2) % 4], make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
           }
         };
-        // A quarter's columns load while the one before is summed; S is free for the next product but
-        // one as soon as the last is in registers.
-        auto done_reading = [&](bool last) {
-          if (!last) return;
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::kBarSFree + 2 * x + buf));
-        };
+        // S is free for the next product but one once this part's columns are in registers.
+        constexpr int kQuarters = 2;  // (one part has 64 columns at most)
 #pragma unroll 1
-        for (int q = 0; q < quarters; q += 2) {
-          tmem_wait_ld_x32(s[0]);
-          done_reading(q + 1 == quarters);
-          if (q + 1 < quarters) tmem_ld_x32(t_b + 32u * (q + 1), s[1]);
-          add(s[0], q);
-          if (q + 1 < quarters) {
-            tmem_wait_ld_x32(s[1]);
-            done_reading(q + 2 == quarters);
-            if (q + 2 < quarters) tmem_ld_x32(t_b + 32u * (q + 2), s[0]);
-            add(s[1], q + 1);
+        for (int q = kQuarters * half; q < kQuarters * (half + 1); ++q) {
+          uint32_t s[32];
+          if (32 * q < cols) {
+            tmem_ld_x32(t_b + 32u * q, s);
+            tmem_wait_ld_x32(s);
           }
+          if (q == kQuarters * (half + 1) - 1) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kBarSFree + 2 * x + buf));
+          }
+          if (32 * q < cols) add(s, q);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kBarColEmpty + cs));
       }
       if (!ok) break;
-      if (key < most && (n > 0 || !p.accumulate)) {
-        const bool skipped = ((bad >> (r_local >> log2T)) & 1u) != 0;
-        const float2 both = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-        const float sum = skipped ? 0.f : both.x + both.y;
+      const float2 both = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+      float sum = both.x + both.y;
+      if (kParts == 2 && n > 0) {
+        // The second half hands its sums to the first, in one of two buffers.
+        const int j = joined % 2;
+        const uint32_t full = bar(L::kBarSumFull + 2 * x + j), free = bar(L::kBarSumFree + 2 * x + j);
+        if (half == 1) {
+          if (!warp_wait(free, parity(joined / 2) ^ 1u)) break;
+          sums_s[j * kMsTile + r_local] = sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        } else {
+          if (!warp_wait(full, parity(joined / 2))) break;
+          sum += sums_s[j * kMsTile + r_local];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(free);
+        }
+        ++joined;
+      }
+      if (half == 0 && key < most && (n > 0 || !p.accumulate)) {
+        if (((bad >> (r_local >> log2T)) & 1u) != 0) sum = 0.f;
         float* dst = p.mass + (static_cast<size_t>(w.b) * p.s.Hkv + w.kvh) * most + key;
         *dst = p.accumulate ? *dst + sum : sum;
       }
@@ -612,7 +636,7 @@ __global__ void __launch_bounds__(kMsThreads, 1)
 
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kIssuer) {
     __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
