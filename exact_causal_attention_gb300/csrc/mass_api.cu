@@ -27,6 +27,9 @@ int launch_mass(const CUtensorMap& tm_q, const CUtensorMap& tm_cache, const eca:
 template <int D, bool BF16>
 int launch_mass_form(const CUtensorMap& tm_q, const CUtensorMap& tm_cache, const eca::MassParams& p, int grid,
                      const Device& dev, cudaStream_t stream) {
+  if (p.f.softcap > 0.f && p.f.slopes != nullptr) {
+    return launch_mass<D, BF16, eca::kFormBoth>(tm_q, tm_cache, p, grid, dev, stream);
+  }
   if (p.f.softcap > 0.f) return launch_mass<D, BF16, eca::kFormCap>(tm_q, tm_cache, p, grid, dev, stream);
   if (p.f.slopes != nullptr) return launch_mass<D, BF16, eca::kFormBias>(tm_q, tm_cache, p, grid, dev, stream);
   return launch_mass<D, BF16, eca::kFormPlain>(tm_q, tm_cache, p, grid, dev, stream);

@@ -14,7 +14,10 @@ namespace eca {
 // Score forms as the kernels' template argument.
 constexpr int kFormPlain = 0;
 constexpr int kFormBias = 1;  // distance bias
-constexpr int kFormCap = 2;   // tanh cap, with or without a bias
+constexpr int kFormCap = 2;   // tanh cap
+constexpr int kFormBoth = 3;  // cap, then bias
+__host__ __device__ constexpr bool form_caps(int form) { return form == kFormCap || form == kFormBoth; }
+__host__ __device__ constexpr bool form_biases(int form) { return form == kFormBias || form == kFormBoth; }
 
 // Scales of the cap: cap_scores gives unit * cap tanh(x scale / cap).
 struct CapScale {
@@ -53,12 +56,16 @@ __device__ __forceinline__ float tanh_wide(float y) {
 }
 
 // A whole warp: 32 scores per thread, x to unit cap tanh(x scale / cap), plus add[i] where
-// there is one (in shared memory, 16-byte aligned, the same for every thread).
-template <bool kAdd>
+// there is one (in shared memory, 16-byte aligned, the same for every thread).  kNear: with
+// the shorter polynomial too (a kernel with much other code does better without it).
+template <bool kAdd, bool kNear>
 __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k, const float* add) {
-  float mx = 0.f;
+  float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) mx = fmax3(mx, fabsf(__uint_as_float(s[i])), fabsf(__uint_as_float(s[i + 1])));
+  for (int i = 0; i < 32; i += 2) {
+    m4[i / 2 % 4] = fmax3(m4[i / 2 % 4], fabsf(__uint_as_float(s[i])), fabsf(__uint_as_float(s[i + 1])));
+  }
+  const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
   auto polynomial = [&](const auto& c) {
     constexpr int kTerms = sizeof(c) / sizeof(float2);
 #pragma unroll
@@ -77,7 +84,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k,
       s[i + 1] = __float_as_uint(a.y);
     }
   };
-  if (__all_sync(0xffffffffu, mx <= k.near)) {
+  if (kNear && __all_sync(0xffffffffu, mx <= k.near)) {
     polynomial(k.n);
   } else if (__all_sync(0xffffffffu, mx <= k.far)) {
     polynomial(k.f);

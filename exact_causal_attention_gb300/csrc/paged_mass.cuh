@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
   } else if (warp == kColumns) {
     // ------------------------------------------------- the columns' values, lane by column
     // (in base 2 with a cap, whose scores come in base 2)
-    const float lse_unit = FORM == kFormCap ? kLog2e : 1.f;
+    const float lse_unit = form_caps(FORM) ? kLog2e : 1.f;
     int tok[4], head[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           dst[lane + 32 * c] = now[c];
-          if (FORM != kFormPlain && p.f.slopes != nullptr) {
+          if constexpr (form_biases(FORM)) {
             dst[kMsCols + lane + 32 * c] = lse_unit * p.f.slopes[(w.kvh * p.chunks + chunk) * p.hc + head[c]];
             dst[2 * kMsCols + lane + 32 * c] = static_cast<float>(w.pos0 + t0 + tok[c]);
           }
@@ -544,9 +544,8 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
         const float* col = cols_s + cs * 3 * kMsCols;
         // Sums 32 columns: 2^(log2e (form(s) - lse)).
         auto add = [&](uint32_t (&v)[32], int q) {
-          if constexpr (FORM == kFormCap) cap_scores<true>(v, cap, col + 32 * q);
+          if constexpr (form_caps(FORM)) cap_scores<true, true>(v, cap, col + 32 * q);
           const float2 c2 = make_float2(p.f.scale, p.f.scale), k2 = make_float2(kLog2e, kLog2e);
-          const bool biased = FORM == kFormBias || (FORM == kFormCap && p.f.slopes != nullptr);
           const bool all = __all_sync(0xffffffffu, lo <= 32 * q && hi >= 32 * q + 32) != 0;
           auto low = [](int m) -> uint32_t { return m <= 0 ? 0u : (m >= 32 ? ~0u : (1u << m) - 1u); };
           const uint32_t seen = low(hi - 32 * q) & ~low(lo - 32 * q);
@@ -554,12 +553,12 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
           for (int i4 = 0; i4 < 32; i4 += 4) {
             float2 y0 = make_float2(__uint_as_float(v[i4]), __uint_as_float(v[i4 + 1]));
             float2 y1 = make_float2(__uint_as_float(v[i4 + 2]), __uint_as_float(v[i4 + 3]));
-            if constexpr (FORM != kFormCap) {
+            if constexpr (!form_caps(FORM)) {
               const float4 z = *reinterpret_cast<const float4*>(col + 32 * q + i4);  // - lse
               y0 = __ffma2_rn(y0, c2, make_float2(z.x, z.y));
               y1 = __ffma2_rn(y1, c2, make_float2(z.z, z.w));
             }
-            if (biased) {
+            if constexpr (form_biases(FORM)) {
               const float4 sl = *reinterpret_cast<const float4*>(col + kMsCols + 32 * q + i4);
               const float4 ps = *reinterpret_cast<const float4*>(col + 2 * kMsCols + 32 * q + i4);
               y0.x = fmaf(-sl.x, fabsf(ps.x - key_f), y0.x);
@@ -567,7 +566,7 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
               y1.x = fmaf(-sl.z, fabsf(ps.z - key_f), y1.x);
               y1.y = fmaf(-sl.w, fabsf(ps.w - key_f), y1.y);
             }
-            if constexpr (FORM != kFormCap) {
+            if constexpr (!form_caps(FORM)) {
               y0 = __fmul2_rn(y0, k2);
               y1 = __fmul2_rn(y1, k2);
             }

@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const int tok = t * p.tq + row_tok;
       const int pos = w.pos + tok;
       float slope2 = 0.f;
-      if (FORM != kFormPlain && p.f.slopes != nullptr && row_ok) slope2 = p.f.slopes[w.head + row_head] * kLog2e;
+      if (form_biases(FORM) && row_ok) slope2 = p.f.slopes[w.head + row_head] * kLog2e;
       float m_ref = -INFINITY;
       float l = 0.f;
       const int first = w.n_max - n_kv;
@@ -763,8 +763,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           uint32_t s[32];
           tmem_ld_x32(t_s + 32u * q, s);
           tmem_wait_ld_x32(s);
-          if constexpr (FORM == kFormCap) cap_scores<false>(s, cap, nullptr);
-          if (FORM == kFormBias || (FORM == kFormCap && p.f.slopes != nullptr)) {
+          if constexpr (form_caps(FORM)) cap_scores<false, false>(s, cap, nullptr);
+          if constexpr (form_biases(FORM)) {
             const float away = static_cast<float>(pos - kb - 32 * q);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -779,8 +779,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               if (!(seen & (1u << i))) s[i] = __float_as_uint(-INFINITY);
             }
           }
+          float t4[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) top = fmax3(top, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          for (int i = 0; i < 32; i += 2) {
+            t4[i / 2 % 4] = fmax3(t4[i / 2 % 4], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          }
+          top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
           if (FORM != kFormPlain || masked) tmem_st_x32(t_s + 32u * q, s);
         }
         top *= c;

@@ -50,6 +50,9 @@ int launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_cache, const e
 template <int D, bool BF16>
 int launch_prefill_form(const CUtensorMap& tm_q, const CUtensorMap& tm_cache, const eca::PrefillParams& p, int grid,
                         const Device& dev, cudaStream_t stream) {
+  if (p.f.softcap > 0.f && p.f.slopes != nullptr) {
+    return launch_prefill<D, BF16, eca::kFormBoth>(tm_q, tm_cache, p, grid, dev, stream);
+  }
   if (p.f.softcap > 0.f) return launch_prefill<D, BF16, eca::kFormCap>(tm_q, tm_cache, p, grid, dev, stream);
   if (p.f.slopes != nullptr) return launch_prefill<D, BF16, eca::kFormBias>(tm_q, tm_cache, p, grid, dev, stream);
   return launch_prefill<D, BF16, eca::kFormPlain>(tm_q, tm_cache, p, grid, dev, stream);
