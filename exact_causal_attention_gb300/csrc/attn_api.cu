@@ -614,8 +614,10 @@ int launch_decode(const CUtensorMap& tm, eca::DecodeParams& p, const DecodeShape
   const long long groups = static_cast<long long>(p.B) * p.Hkv * sh.head_chunks;
   long long ctas = groups * sh.splits;
   if (FORM) {
-    // Segments of one size for all requests: rounding up adds at most one CTA per group.
-    if (ctas > p.target + groups) ctas = p.target + groups;
+    // Segments of one size for all requests, at least 1 / kDecMostWaves of the even share: rounding up
+    // adds at most one CTA per group.
+    const long long bound = eca::kDecMostWaves * static_cast<long long>(p.target) + groups;
+    if (ctas > bound) ctas = bound;
   }
   if (ctas > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   const unsigned grid = static_cast<unsigned>(ctas);

@@ -102,29 +102,47 @@ __device__ __forceinline__ int decode_length(const DecodeParams& p, int b) {
 
 // How the FORM instances cut the contexts into segments: all of one size (in tiles of
 // kDecTile tokens), so that a long request gets more of them than a short one and every CTA about the
-// same work.  About p.target CTAs in all, and no more than p.splits segments a request.
+// same work, and no more than p.splits segments a request.  p.target CTAs run at once; up to 32 requests,
+// the size is the one of 32 candidates with the fewest waves of CTAs times (tiles + the cost of starting and
+// ending a segment): one CTA too many for a wave can cost a half (32 requests with a window of 4096: 124 us
+// with the even share, 95 with a third more segments).
 // Called by a whole warp, which reads every length (32 at a time).
-struct DecodeCut {
-  int tiles;  // of a segment
-};
-
+constexpr int kDecSegCost = 3;        // of starting and ending a segment, in tiles
+constexpr int kDecMostWaves = 3;      // candidates are at least the even share / kDecMostWaves
 __device__ __forceinline__ int decode_tiles(const DecodeParams& p, int b, int log2T) {
   const int per_tile = kDecTile >> log2T;
   return (decode_pages(p, b, decode_length(p, b), log2T).n + per_tile - 1) / per_tile;
 }
 
-__device__ __forceinline__ DecodeCut decode_cut(const DecodeParams& p, int log2T) {
+// The tiles of a segment; `mine` gets the tiles of request `lane` where there are 32 at most.
+__device__ __forceinline__ int decode_cut(const DecodeParams& p, int log2T, int* mine) {
+  const int lane = static_cast<int>(threadIdx.x % 32);
+  const int heads = p.Hkv * p.head_chunks;
   long long total = 0;
   int most = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + static_cast<int>(threadIdx.x % 32);
-    const int t = b < p.B ? decode_tiles(p, b, log2T) : 0;
+    const int t = b0 + lane < p.B ? decode_tiles(p, b0 + lane, log2T) : 0;
     most = max(most, __reduce_max_sync(0xffffffffu, t));
     total += __reduce_add_sync(0xffffffffu, t);
+    *mine = t;
   }
-  const long long even = (total * p.Hkv * p.head_chunks + p.target - 1) / p.target;
-  const int least = (most + p.splits - 1) / p.splits;
-  return DecodeCut{max(1, max(static_cast<int>(even), least))};
+  const int even = static_cast<int>((total * heads + p.target - 1) / p.target);
+  const int least = max(1, (most + p.splits - 1) / p.splits);
+  if (p.B > 32) return max(even, least);
+  // Candidate sizes of lane i: (6 + i) / 16 of the even share.  (Counted in fp32: any size will do,
+  // as long as every CTA picks the same.)
+  const int size = max(least, static_cast<int>((static_cast<long long>(even) * (6 + lane) + 15) / 16));
+  const float inv = __frcp_rn(static_cast<float>(size));
+  float count = 0.f;
+  for (int b = 0; b < p.B; ++b) {
+    count += fmaxf(1.f, ceilf(static_cast<float>(__shfl_sync(0xffffffffu, *mine, b)) * inv));
+  }
+  const float waves = ceilf(count * static_cast<float>(heads) / static_cast<float>(p.target));
+  const float cost = waves * static_cast<float>(size + kDecSegCost);
+  // The lowest cost, then the smallest size: lanes are in order of size.  (Positive floats order as integers.)
+  const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));
+  const int who = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(cost) == best)) - 1;
+  return __shfl_sync(0xffffffffu, size, who);
 }
 
 // Bits 0 .. n - 1.
@@ -231,14 +249,16 @@ __global__ void __maxnreg__(128) paged_decode_kernel(const __grid_constant__ CUt
   if constexpr (FORM) {
     // unit: (b, segment, kv head, head chunk), the heads of a segment (contiguous in memory) side by side
     const int form_log2T = 31 - __clz(p.page_size);
-    seg_tiles = decode_cut(p, form_log2T).tiles;
+    int tiles = 0;
+    seg_tiles = decode_cut(p, form_log2T, &tiles);
     const int heads = p.Hkv * p.head_chunks;
     b = p.B;
     int before = 0;  // CTAs of the requests before
     for (int b0 = 0; b0 < p.B && b == p.B; b0 += 32) {
       const int mine = b0 + lane;
       // An empty request has one segment, which writes its output.
-      const int n = mine < p.B ? max(1, (decode_tiles(p, mine, form_log2T) + seg_tiles - 1) / seg_tiles) * heads : 0;
+      if (p.B > 32) tiles = mine < p.B ? decode_tiles(p, mine, form_log2T) : 0;
+      const int n = mine < p.B ? max(1, (tiles + seg_tiles - 1) / seg_tiles) * heads : 0;
       int upto = n;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -682,7 +702,8 @@ __global__ void __launch_bounds__(256) paged_decode_combine(const DecodeParams p
     if constexpr (FORM) {
       const int log2T = 31 - __clz(p.page_size);
       n_pages = decode_pages(p, b, len, log2T).n;
-      seg_pages = decode_cut(p, log2T).tiles * (kDecTile >> log2T);
+      int tiles;
+      seg_pages = decode_cut(p, log2T, &tiles) * (kDecTile >> log2T);
     }
     const int valid = min(p.splits, (n_pages + seg_pages - 1) / seg_pages);
     const size_t stride = static_cast<size_t>(p.B) * p.Hq;
