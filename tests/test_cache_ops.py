@@ -141,6 +141,29 @@ def test_mass_with_bad_pages_and_rows_without_keys(cuda_lib):
     near(got, want, tol)
 
 
+@pytest.mark.gpu
+def test_mass_repeats_and_replays_bit_identically(cuda_lib):
+    eca = cuda_lib
+    q, cache, table, lens, offsets, dtype, T, form, lse = plain_lse("long_context")
+    args = [x.cuda() for x in (q, lse, cache, table, lens, offsets)]
+    want = eca.paged_attn_mass(*args)
+    mass = torch.zeros_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mass.zero_()
+        eca.paged_attn_mass(*args, mass=mass)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(mass, want)
+        with torch.cuda.stream(side):
+            again = eca.paged_attn_mass(*args)
+        torch.cuda.synchronize()
+        assert torch.equal(again, want)
+    assert eca.device_status() == 0
+
+
 # ------------------------------------------------------------------------------- eviction
 
 EVICT = {

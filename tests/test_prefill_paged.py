@@ -261,6 +261,129 @@ def test_calls_at_once_on_two_streams(cuda_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,splits", [(40, None), (40, 6), (520, 10)])
+def test_decode_form_of_many_requests(cuda_lib, B, splits):
+    """More than 32 requests (the segments' size is then the even share), and more groups than the
+    in-kernel merge has counters for (520 x 8), merged by the second kernel."""
+    eca = cuda_lib
+    Hq, Hkv, D, T = 8, 8, 64, 64
+    rng = np.random.default_rng(6)
+    lengths = [int(x) for x in rng.integers(1, 641, size=B)]
+    lengths[0] = 640
+    q, cache, table, lens, offsets = ref.chunk(B, Hq, Hkv, D, T, [(1, L) for L in lengths], "fp16", 93)
+    form = dict(slopes=torch.exp2(-torch.arange(1, Hq + 1, dtype=torch.float32)), window=300,
+                prefix=torch.from_numpy(rng.integers(0, 40, size=B).astype(np.int32)))
+    out, lse = eca.decode_paged(q.cuda(), cache.cuda(), table.cuda(), lens.cuda(), kv_splits=splits, **to_call(form))
+    assert eca.device_status() == 0
+    o, l, tol_o, tol_l = ref.attention(q, cache, table, lens, offsets, T, "fp16", 1.0 / math.sqrt(D), **form)
+    near(lse, l, tol_l)
+    near(out, o, tol_o)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_std,cap", [(300.0, 5.0), (0.01, 50.0), (40.0, 30.0)])
+def test_cap_of_scores_far_beyond_and_far_below_it(cuda_lib, q_std, cap):
+    eca = cuda_lib
+    q, cache, table, lens, offsets = ref.chunk(2, 8, 2, 128, 16, [(50, 260), (1, 300)], "bf16", 17, q_std)
+    o, l, tol_o, tol_l = ref.attention(q, cache, table, lens, offsets, 16, "bf16", 1.0 / math.sqrt(128), softcap=cap)
+    out, lse = eca.prefill_paged(q.cuda(), cache.cuda(), table.cuda(), lens.cuda(), offsets.cuda(), softcap=cap)
+    assert eca.device_status() == 0
+    near(lse, l, tol_l)
+    near(out, o, tol_o)
+
+
+@pytest.mark.gpu
+def test_workspace_contents_do_not_matter(cuda_lib):
+    eca = cuda_lib
+    for name in ("long_context", "window_sinks", "everything"):
+        q, cache, table, lens, offsets, dtype, T, form = case_inputs(name)
+        g = [x.cuda() for x in (q, cache, table, lens, offsets)]
+        want = eca.prefill_paged(*g, **to_call(form))
+        need = eca.prefill_workspace_bytes(q.shape[0], lens.shape[0], q.shape[1], cache.shape[3], q.shape[2], T, table.shape[1])
+        for fill in (0, 255):  # 255: NaN as fp32, -1 as int32
+            ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+            got = eca.prefill_paged(*g, workspace=ws, **to_call(form))
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+def test_two_graphs_at_once(cuda_lib):
+    """Graphs captured with workspaces of their own, replayed side by side."""
+    eca = cuda_lib
+    graphs, outs, want = [], [], []
+    for name in ("long_context", "chunk_ends_in_tile"):
+        q, cache, table, lens, offsets, dtype, T, form = case_inputs(name)
+        g = [x.cuda() for x in (q, cache, table, lens, offsets)]
+        want.append(eca.prefill_paged(*g))
+        out, lse = torch.empty_like(want[-1][0]), torch.empty_like(want[-1][1])
+        need = eca.prefill_workspace_bytes(q.shape[0], lens.shape[0], q.shape[1], cache.shape[3], q.shape[2], T, table.shape[1])
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(4):
+                eca.prefill_paged(*g, out=out, lse=lse, workspace=ws)
+        graphs.append((graph, g, ws))
+        outs.append((out, lse))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(3):
+        for stream, (graph, _, _) in zip(streams, graphs):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert eca.device_status() == 0
+    for (o, l), (wo, wl) in zip(outs, want):
+        assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+@pytest.mark.gpu
+def test_whole_prompt_is_the_dense_forward(cuda_lib):
+    """A prompt in one chunk, long enough that every CTA takes parts of several units, against the
+    dense kernel on the same values (whose own error against 64 bits the parity tests bound)."""
+    eca = cuda_lib
+    N, Hq, Hkv, D, T = 3000, 16, 4, 128, 16
+    g = torch.Generator(device="cuda").manual_seed(21)
+    q, k, v = (torch.randn(N, h, D, generator=g, device="cuda").half() for h in (Hq, Hkv, Hkv))
+    pages = -(-N // T)
+    table = torch.randperm(pages + 5, generator=torch.Generator().manual_seed(3))[:pages].to(torch.int32).cuda()[None]
+    cache = torch.full((pages + 5, 2, T, Hkv, D), float("nan"), dtype=torch.float16, device="cuda")
+    lens = torch.tensor([N], dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, N], dtype=torch.int32, device="cuda")
+    eca.paged_append_chunk(torch.stack([k, v], 1).contiguous(), cache, table, lens, offsets)
+    out, lse = eca.prefill_paged(q, cache, table, lens, offsets)
+    do, dl = eca.attn_fwd_gqa(*(x.permute(1, 0, 2)[None].contiguous() for x in (q, k, v)))
+    assert eca.device_status() == 0
+    do, dl = do[0].permute(1, 0, 2), dl[0].permute(1, 0)
+    # Both sides' lse within 1e-4 of the exact one; both round P and O to fp16: u (A + |O|) each, and
+    # A = sum p |v| / l is at most the largest |v| of the head.
+    assert (lse - dl).abs().max() <= 2e-4
+    bound = 2 * (ref.HALF["fp16"] * (v.abs().amax().float() + do.abs().float()) + 2.0 ** -25 * v.abs().float().sum(0).amax())
+    assert ((out.float() - do.float()).abs() <= bound).all()
+    assert (out.float() - do.float()).abs().mean() <= 2 * ref.HALF["fp16"] * do.abs().float().mean() + 1e-5
+
+
+@pytest.mark.gpu
+def test_nothing_to_do(cuda_lib):
+    """No rows at all, and requests that bring none."""
+    eca = cuda_lib
+    cache = torch.zeros(4, 2, 16, 2, 64, dtype=torch.float16, device="cuda")
+    table = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([20, 0], dtype=torch.int32, device="cuda")
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")
+    q = torch.empty(0, 4, 64, dtype=torch.float16, device="cuda")
+    out, lse = eca.prefill_paged(q, cache, table, lens, none)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    eca.paged_append_chunk(torch.empty(0, 2, 2, 64, dtype=torch.float16, device="cuda"), cache, table, lens, none)
+    mass = eca.paged_attn_mass(q, lse, cache, table, lens, none)
+    assert torch.all(mass == 0)
+    spare = torch.full((5, 4, 64), 3.0, dtype=torch.float16, device="cuda")  # rows of no request
+    out, lse = torch.full_like(spare, 7.0), torch.full((5, 4), 7.0, device="cuda")
+    eca.prefill_paged(spare, cache, table, lens, none, out=out, lse=lse)
+    mass = eca.paged_attn_mass(spare, lse, cache, table, lens, none, mass=mass + 1.0)
+    assert eca.device_status() == 0
+    assert torch.all(out == 7.0) and torch.all(lse == 7.0) and torch.all(mass == 1.0)
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits(cuda_lib):
     """A cache of more than 2^31 elements (4 GiB and more), the pages in use at its far end."""
     eca = cuda_lib
