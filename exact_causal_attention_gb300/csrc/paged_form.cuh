@@ -4,9 +4,11 @@
 // would treble the work of the unit that the softmax's own exponential needs.  Scores are
 // mostly well inside the cap, where tanh(y) = y P(y^2) takes multiply-adds alone: P is a
 // polynomial fitted to tanh(y) / y by iteratively reweighted least squares, of degree 5 on
-// |y| <= 0.75 or 7 on |y| <= 1.25 (relative errors 3e-8 and 8e-8 before rounding).  A group of scores
-// with one outside takes the exponential.
+// |y| <= 0.75 or 7 on |y| <= 1.25 (relative errors 3e-8 and 8e-8 before rounding).  In a group of
+// scores with some outside those take the exponential.
 #pragma once
+#include <type_traits>
+
 #include "paged_common.cuh"
 
 namespace eca {
@@ -21,8 +23,8 @@ __host__ __device__ constexpr bool form_biases(int form) { return form == kFormB
 
 // Scales of the cap: cap_scores gives unit * cap tanh(x scale / cap).
 struct CapScale {
-  float in;     // scale / cap
-  float out;    // cap unit
+  float out;        // cap unit
+  float wide;       // 2 log2e scale / cap
   float near, far;  // |x| up to which the shorter and the longer polynomial hold
   // Their coefficients for x^2, with the scales folded in, for pairs of scores.
   float2 n[6], f[8];
@@ -34,30 +36,34 @@ __device__ __forceinline__ CapScale cap_scale(float scale, float softcap, float 
   constexpr float kFarCoef[8] = {0.99999994f,    -0.333327f,     0.13324507f,    -0.05349034f,
                                  0.020557173f, -0.0067961547f, 0.0015881141f, -0.00018259805f};
   CapScale r;
-  r.in = softcap > 0.f ? scale / softcap : 0.f;
+  const float in = softcap > 0.f ? scale / softcap : 0.f;
   r.out = softcap * unit;
-  r.near = r.in > 0.f ? kNear / r.in : 0.f;
-  r.far = r.in > 0.f ? kFar / r.in : 0.f;
+  r.wide = 2.f * kLog2e * in;
+  r.near = in > 0.f ? kNear / in : 0.f;
+  r.far = in > 0.f ? kFar / in : 0.f;
   float f = scale * unit;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (i < 6) r.n[i] = make_float2(kNearCoef[i] * f, kNearCoef[i] * f);
     r.f[i] = make_float2(kFarCoef[i] * f, kFarCoef[i] * f);
-    f *= r.in * r.in;
+    f *= in * in;
   }
   return r;
 }
 
-// tanh(y) = 1 - 2 / (1 + e^2y), for any y.
-__device__ __forceinline__ float tanh_wide(float y) {
+// out tanh(x in) + plus by tanh(y) = 1 - 2 / (1 + e^2y), for x that is not small.  `plus` joins the
+// leading term, so that where the sum is small its rounding is too.
+__device__ __forceinline__ float cap_wide(float x, const CapScale& k, float plus) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(y * (2.f * kLog2e)) + 1.f));
-  return fmaf(-2.f, r, 1.f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(fabsf(x) * k.wide) + 1.f));
+  const float side = copysignf(k.out, x);
+  return fmaf(-2.f * side, r, side + plus);
 }
 
 // A whole warp: 32 scores per thread, x to unit cap tanh(x scale / cap), plus add[i] where
 // there is one (in shared memory, 16-byte aligned, the same for every thread).  kNear: with
-// the shorter polynomial too (a kernel with much other code does better without it).
+// the shorter polynomial, and the longer one in mixed groups too; a kernel whose warps wait for
+// instructions does better without (a mixed step's chunk attention: 209 us, with them 227).
 template <bool kAdd, bool kNear>
 __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k, const float* add) {
   float m4[4] = {0.f, 0.f, 0.f, 0.f};
@@ -66,7 +72,8 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k,
     m4[i / 2 % 4] = fmax3(m4[i / 2 % 4], fabsf(__uint_as_float(s[i])), fabsf(__uint_as_float(s[i + 1])));
   }
   const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-  auto polynomial = [&](const auto& c) {
+  // all: each score that lies outside the polynomial's range takes the exponential instead.
+  auto polynomial = [&](const auto& c, auto all) {
     constexpr int kTerms = sizeof(c) / sizeof(float2);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
@@ -75,25 +82,31 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k,
       float2 a = c[kTerms - 1];
 #pragma unroll
       for (int j = kTerms - 2; j >= 0; --j) a = __ffma2_rn(a, z, c[j]);
+      float2 plus = make_float2(0.f, 0.f);
+      if constexpr (kAdd) plus = *reinterpret_cast<const float2*>(add + i);
       if constexpr (kAdd) {
-        a = __ffma2_rn(a, x, *reinterpret_cast<const float2*>(add + i));
+        a = __ffma2_rn(a, x, plus);
       } else {
         a = __fmul2_rn(a, x);
+      }
+      if constexpr (decltype(all)::value) {
+        if (!(fabsf(x.x) <= k.far)) a.x = cap_wide(x.x, k, plus.x);
+        if (!(fabsf(x.y) <= k.far)) a.y = cap_wide(x.y, k, plus.y);
       }
       s[i] = __float_as_uint(a.x);
       s[i + 1] = __float_as_uint(a.y);
     }
   };
   if (kNear && __all_sync(0xffffffffu, mx <= k.near)) {
-    polynomial(k.n);
+    polynomial(k.n, std::false_type{});
   } else if (__all_sync(0xffffffffu, mx <= k.far)) {
-    polynomial(k.f);
+    polynomial(k.f, std::false_type{});
+  } else if constexpr (kNear) {
+    polynomial(k.f, std::true_type{});
   } else {
+    // All of them by the exponential: off by 3e-7 of the cap at small scores, in a quarter of the code.
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float t = tanh_wide(__uint_as_float(s[i]) * k.in);
-      s[i] = __float_as_uint(kAdd ? fmaf(k.out, t, add[i]) : k.out * t);
-    }
+    for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(cap_wide(__uint_as_float(s[i]), k, kAdd ? add[i] : 0.f));
   }
 }
 

@@ -19,8 +19,8 @@
 // per slot, so the next product does not wait for the sums.
 //
 // e^(s - lse) is taken as 2^(log2e (s - lse)) with the difference formed first in natural units: where
-// the weight matters s is near lse, so the one rounding of the difference is small.  (With a cap both are
-// in base 2 from the start: its own error is larger, and the difference then costs nothing.)
+// the weight matters s is near lse, so the one rounding of the difference is small.  (In base 2 from the
+// start the rounding of lse and of the cap would each cost 1e-6 of the weights.)
 #pragma once
 #include <cuda.h>
 
@@ -421,8 +421,6 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
     }
   } else if (warp == kColumns) {
     // ------------------------------------------------- the columns' values, lane by column
-    // (in base 2 with a cap, whose scores come in base 2)
-    const float lse_unit = form_caps(FORM) ? kLog2e : 1.f;
     int tok[4], head[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -443,7 +441,7 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
           next[c] = -INFINITY;
           if (tok[c] < p.tq && t0 + tok[c] < w.n) {
             const float z = p.lse[static_cast<size_t>(w.row0 + t0 + tok[c]) * p.Hq + (w.kvh * p.chunks + chunk) * p.hc + head[c]];
-            next[c] = z == -INFINITY ? z : -z * lse_unit;
+            next[c] = z == -INFINITY ? z : -z;
           }
         }
       };
@@ -464,7 +462,7 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
         for (int c = 0; c < 4; ++c) {
           dst[lane + 32 * c] = now[c];
           if constexpr (form_biases(FORM)) {
-            dst[kMsCols + lane + 32 * c] = lse_unit * p.f.slopes[(w.kvh * p.chunks + chunk) * p.hc + head[c]];
+            dst[kMsCols + lane + 32 * c] = p.f.slopes[(w.kvh * p.chunks + chunk) * p.hc + head[c]];
             dst[2 * kMsCols + lane + 32 * c] = static_cast<float>(w.pos0 + t0 + tok[c]);
           }
         }
@@ -480,7 +478,7 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
     const uint32_t t_s = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + 256u * x;
     const int log2T = 31 - __clz(p.s.page_size);
     auto warp_wait = [&](uint32_t b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, wd.wait(b, ph)) != 0; };
-    const CapScale cap = cap_scale(p.f.scale, p.f.softcap, kLog2e);
+    const CapScale cap = cap_scale(p.f.scale, p.f.softcap, 1.f);
     float* sums_s = reinterpret_cast<float*>(smem + L::kSumOff) + 2 * x * kMsTile;
     int it = 0, step = 0, uses = 0;
     int joined = 0;  // units of this slot whose halves were joined
@@ -566,10 +564,8 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
               y1.x = fmaf(-sl.z, fabsf(ps.z - key_f), y1.x);
               y1.y = fmaf(-sl.w, fabsf(ps.w - key_f), y1.y);
             }
-            if constexpr (!form_caps(FORM)) {
-              y0 = __fmul2_rn(y0, k2);
-              y1 = __fmul2_rn(y1, k2);
-            }
+            y0 = __fmul2_rn(y0, k2);
+            y1 = __fmul2_rn(y1, k2);
             v[i4] = __float_as_uint(ex2(y0.x));
             v[i4 + 1] = __float_as_uint(ex2(y0.y));
             v[i4 + 2] = __float_as_uint(ex2(y1.x));
