@@ -667,6 +667,10 @@ int decode_impl(bool bf16, const void* q, const void* cache, const int* block_ta
   if (kv_splits < 1 || kv_splits > kMaxSplits) return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4))) return ATTN_ERR_UNALIGNED;
   if (!std::isfinite(softcap) || softcap < 0.f || window < 0) return ATTN_ERR_INVALID_ARG;
+  // (the score forms count positions a little past the longest context)
+  if ((softcap > 0.f || window > 0 || slopes) && static_cast<uint64_t>(max_pages) * page_size > 0x7fffffffull - 512) {
+    return ATTN_ERR_INVALID_ARG;
+  }
   if ((slopes && !aligned(slopes, 4)) || (prefix && !aligned(prefix, 4))) return ATTN_ERR_UNALIGNED;
   const uint64_t qbytes = static_cast<uint64_t>(B) * Hq * D * 2;
   if (overlaps(out, qbytes, q, qbytes)) return ATTN_ERR_INVALID_ARG;

@@ -11,6 +11,7 @@ int attn_paged_append_chunk(const void* new_kv, void* cache, const int* block_ta
                             const int* q_offsets, int total, int B, int Hkv, int D, int page_size, int max_pages,
                             int num_pages, attn_stream_t stream) {
   int rc = check_paged_args(cache, block_table, lengths, B, Hkv, D, page_size, max_pages, num_pages);
+  if (rc == ATTN_OK) rc = check_positions(page_size, max_pages);
   if (rc != ATTN_OK) return rc;
   if (total < 0 || !q_offsets || (!new_kv && total > 0)) return ATTN_ERR_INVALID_ARG;
   if (!aligned(new_kv, 16) || !aligned(q_offsets, 4)) return ATTN_ERR_UNALIGNED;
@@ -35,6 +36,7 @@ int attn_paged_evict(void* cache, const int* block_table, const int* lengths, co
                      int* new_lengths, float* mass_out, int B, int Hkv, int D, int page_size, int max_pages,
                      int num_pages, int budget, int recent, attn_stream_t stream) {
   int rc = check_paged_args(cache, block_table, lengths, B, Hkv, D, page_size, max_pages, num_pages);
+  if (rc == ATTN_OK) rc = check_positions(page_size, max_pages);
   if (rc != ATTN_OK) return rc;
   if (!mass || !kept || !new_lengths) return ATTN_ERR_INVALID_ARG;
   if (budget < 1 || budget > max_pages * page_size || recent < 0 || recent > budget) return ATTN_ERR_INVALID_ARG;

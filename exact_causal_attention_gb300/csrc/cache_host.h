@@ -34,6 +34,11 @@ inline uint64_t cache_bytes(int Hkv, int D, int page_size, int num_pages) {
   return static_cast<uint64_t>(num_pages) * 2 * page_size * Hkv * D * 2;
 }
 
+// Positions are counted up to two key tiles past the longest context in an int.
+inline int check_positions(int page_size, int max_pages) {
+  return static_cast<uint64_t>(max_pages) * page_size > 0x7fffffffull - 512 ? ATTN_ERR_INVALID_ARG : ATTN_OK;
+}
+
 // Query-side arguments of the chunk operators.
 inline int check_chunk_args(const void* q, int total, int Hq, int Hkv, int D, float scale, float softcap, int window,
                      const float* slopes, const int* prefix) {

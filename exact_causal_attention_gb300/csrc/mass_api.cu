@@ -40,6 +40,7 @@ int mass_impl(bool bf16, const void* q, const float* lse, const void* cache, con
               int Hkv, int D, int page_size, int max_pages, int num_pages, float scale, float softcap, int window,
               const float* alibi_slopes, const int* prefix_lens, attn_stream_t stream) {
   int rc = check_paged_args(cache, block_table, lengths, B, Hkv, D, page_size, max_pages, num_pages);
+  if (rc == ATTN_OK) rc = check_positions(page_size, max_pages);
   if (rc == ATTN_OK) rc = check_chunk_args(q, total_q, Hq, Hkv, D, scale, softcap, window, alibi_slopes, prefix_lens);
   if (rc != ATTN_OK) return rc;
   if (!mass || (!lse && total_q > 0) || (!q_offsets && total_q != B)) return ATTN_ERR_INVALID_ARG;

@@ -64,6 +64,7 @@ int prefill_impl(bool bf16, const void* q, const void* cache, const int* block_t
                  const float* alibi_slopes, const int* prefix_lens, void* workspace, size_t workspace_bytes,
                  attn_stream_t stream) {
   int rc = check_paged_args(cache, block_table, lengths, B, Hkv, D, page_size, max_pages, num_pages);
+  if (rc == ATTN_OK) rc = check_positions(page_size, max_pages);
   if (rc == ATTN_OK) rc = check_chunk_args(q, total_q, Hq, Hkv, D, scale, softcap, window, alibi_slopes, prefix_lens);
   if (rc != ATTN_OK) return rc;
   if (!q_offsets || (!out && total_q > 0) || B > eca::kPlanMaxRequests) return ATTN_ERR_INVALID_ARG;

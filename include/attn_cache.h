@@ -9,7 +9,7 @@
  * status codes and attn_device_status holds here.  The cache's layout is that of
  * attn_decode_paged: [num_pages, 2, page_size, Hkv, D] 16-bit (index 0 = K, 1 = V),
  * block_table [B, max_pages] int32, lengths [B] int32, page_size 8, 16, 32 or 64, D 64
- * or 128, num_pages * 2 * page_size < 2^31 and max_pages * page_size < 2^31.
+ * or 128, num_pages * 2 * page_size < 2^31 and max_pages * page_size < 2^31 - 512.
  *
  * A ragged chunk of new tokens: request b owns rows q_offsets[b] .. q_offsets[b + 1] - 1
  * of the packed tensors, n_b of them, and lengths[b] counts its whole context with
@@ -106,7 +106,7 @@ int attn_paged_append_chunk(const void* new_kv, void* cache, const int* block_ta
  *   mass         : device, [B, Hkv, max_pages * page_size] fp32.  accumulate = 0 writes it
  *                  in full (0 where no row looks); otherwise it is added to, and
  *                  places that no row looks at are left alone.
- * The other arguments as attn_prefill_paged.  Sums are taken in fp32 in a fixed order:
+ * The other arguments as attn_prefill_paged (B up to 4096).  Sums are taken in fp32 in a fixed order:
  * the same call gives the same bits.
  */
 int attn_paged_mass(const void* q, const float* lse, const void* cache, const int* block_table,

@@ -361,6 +361,8 @@ def test_mass_refusals_without_a_gpu(lib):
         assert c(cap=-1.0) == -1
         assert c(window=-1) == -1
         assert c(scale=math.inf) == -1
+        assert c(B=4097, total=4097, offsets=None) == -1
+        assert c(mp=(1 << 27) - 8, B=1) == -1  # positions up to 2^31 - 128
         assert c(mass=A + 2) == -2
         assert c(lse=A + SZ + 2) == -2
         assert c(q=A + 8) == -2
@@ -379,6 +381,7 @@ def test_evict_refusals_without_a_gpu(lib):
         assert c(**{name: None}) == -1, name
     assert c(budget=0) == -1
     assert c(budget=65) == -1  # past max_pages * page_size
+    assert c(mp=(1 << 27) - 8, B=1) == -1  # positions up to 2^31 - 128
     assert c(recent=-1) == -1
     assert c(recent=33) == -1
     assert c(D=96) == -3

@@ -454,6 +454,8 @@ def test_refusals_without_a_gpu(lib, fn):
     refused(-1, out=A + 16)           # over q
     refused(-1, out=A + SZ + 64)      # over the cache
     refused(-1, P=1 << 27)            # 2^32 token rows
+    refused(-1, mp=(1 << 27) - 8, T=16, B=1)  # positions up to 2^31 - 128
+    refused(-1, B=4097)
     refused(-1, total=1 << 30)        # (row, head) pairs past an int
     assert c_call(lib, fn, total=0, q=None, out=None, lse=None) == 0
     need = lib.attn_prefill_workspace_bytes(64, 2, 8, 2, 128, 16, 16)
