@@ -25,11 +25,13 @@ int attn_paged_append_chunk(const void* new_kv, void* cache, const int* block_ta
   if (rc != ATTN_OK) return rc;
   const eca::ChunkShape s =
       chunk_shape(block_table, lengths, q_offsets, total, B, Hkv, D, page_size, max_pages, num_pages, dev.status);
-  const long long vecs = static_cast<long long>(total) * 2 * Hkv * D / 8;
-  const long long want = (vecs + eca::kAppendThreads - 1) / eca::kAppendThreads, cap = dev.sm_count * 8LL;
+  // A few tokens a block where that still fills the GPU.
+  const int tokens = total >= 2 * dev.sm_count * eca::kAppendTokens ? eca::kAppendTokens : 1;
+  const long long want = (total + tokens - 1LL) / tokens, cap = dev.sm_count * 8LL;
   return launched(launch_pdl(eca::paged_append_chunk_kernel, static_cast<unsigned>(want < cap ? want : cap),
                              eca::kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream),
-                             static_cast<const uint4*>(new_kv), static_cast<uint4*>(cache), s));
+                             static_cast<const uint4*>(new_kv), static_cast<uint4*>(cache), s,
+                             eca::make_fast_div(Hkv * D / 8), tokens));
 }
 
 int attn_paged_evict(void* cache, const int* block_table, const int* lengths, const float* mass, int* kept,
