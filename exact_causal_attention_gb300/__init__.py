@@ -104,6 +104,8 @@ def library_path() -> str:
 def load_library(path: str | None = None):
     """Load the CUDA library (built by ``exact_causal_attention_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or _LIB_PATH
@@ -330,23 +332,36 @@ def row_softmax(x, out=None, stream=None):
     return out
 
 
-def _check_cache(cache, block_table, lengths, B: int):
-    """Checks a paged cache with its table and lengths; returns (P, T, Hkv, D, max_pages)."""
-    import torch
+_torch_module = None
 
-    if cache.dim() != 5 or cache.shape[1] != 2 or cache.dtype not in (torch.float16, torch.bfloat16):
+
+def _torch():
+    """torch, imported on first use (an import statement costs a fraction of a microsecond per call)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
+
+
+def _check_cache(torch, cache, block_table, lengths):
+    """Checks a paged cache with its table and lengths; returns (P, T, Hkv, D, B, max_pages, dtype,
+    device index)."""
+    shape, table, dt, dev = cache.shape, block_table.shape, cache.dtype, cache.get_device()
+    if len(shape) != 5 or shape[1] != 2 or not (dt is torch.float16 or dt is torch.bfloat16):
         raise ValueError("cache must be [P, 2, T, Hkv, D] float16 or bfloat16")
-    if block_table.dim() != 2 or block_table.shape[0] != B or lengths.shape != (B,):
+    if len(table) != 2 or lengths.shape != table[:1]:
         raise ValueError("block_table must be [B, max_pages] and lengths [B]")
-    if block_table.dtype != torch.int32 or lengths.dtype != torch.int32:
+    if block_table.dtype is not torch.int32 or lengths.dtype is not torch.int32:
         raise ValueError("block_table and lengths must be int32")
-    dev = cache.get_device()
     if dev < 0 or block_table.get_device() != dev or lengths.get_device() != dev:
         raise ValueError("cache, block_table and lengths must be CUDA tensors on one device")
     if not (cache.is_contiguous() and block_table.is_contiguous() and lengths.is_contiguous()):
         raise ValueError("cache, block_table and lengths must be contiguous")
-    P, _, T, Hkv, D = cache.shape
-    return P, T, Hkv, D, block_table.shape[1]
+    P, _, T, Hkv, D = shape
+    B, max_pages = table
+    return P, T, Hkv, D, B, max_pages, dt, dev
 
 
 def _check_like(name: str, t, shape, dtype, dev: int) -> None:
@@ -357,14 +372,12 @@ def _check_like(name: str, t, shape, dtype, dev: int) -> None:
 
 def _form_ptrs(alibi_slopes, prefix_lens, Hq: int, B: int, dev: int):
     """Pointers of the optional per-head slopes [Hq] and per-request prefixes [B]."""
-    import torch
-
     slopes = prefix = None
     if alibi_slopes is not None:
-        _check_like("alibi_slopes", alibi_slopes, (Hq,), torch.float32, dev)
+        _check_like("alibi_slopes", alibi_slopes, (Hq,), _torch().float32, dev)
         slopes = alibi_slopes.data_ptr()
     if prefix_lens is not None:
-        _check_like("prefix_lens", prefix_lens, (B,), torch.int32, dev)
+        _check_like("prefix_lens", prefix_lens, (B,), _torch().int32, dev)
         prefix = prefix_lens.data_ptr()
     return slopes, prefix
 
@@ -372,12 +385,10 @@ def _form_ptrs(alibi_slopes, prefix_lens, Hq: int, B: int, dev: int):
 def _workspace(workspace, need: int, dev: int):
     """(pointer, bytes) of the caller's workspace, or of a new 256-byte aligned one, and
     the tensor that holds it."""
-    import torch
-
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need + 256, dtype=torch.uint8, device=f"cuda:{dev}")
+        workspace = _torch().empty(need + 256, dtype=_torch().uint8, device=f"cuda:{dev}")
         ptr = workspace.data_ptr()
         return ptr + (-ptr) % 256, need, workspace
     if workspace.get_device() != dev or not workspace.is_contiguous():
@@ -385,21 +396,13 @@ def _workspace(workspace, need: int, dev: int):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-class _on_device:
-    """``torch.cuda.device(dev)`` that costs nothing when ``dev`` is current already."""
-
-    def __init__(self, dev: int):
-        import torch
-
-        self.guard = None if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(dev: int, fn, *args) -> int:
+    """``fn(*args)`` with CUDA device ``dev`` current."""
+    torch = _torch()
+    if torch._C._cuda_getDevice() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def decode_paged(q, cache, block_table, lengths, scale: float | None = None, kv_splits: int | None = None,
@@ -410,8 +413,7 @@ def decode_paged(q, cache, block_table, lengths, scale: float | None = None, kv_
     (``softcap``: cap * tanh(s / cap)), biased by distance (``alibi_slopes`` [Hq] float32) and
     limited to the last ``window`` tokens, with the first ``prefix_lens`` [B] int32 tokens
     visible whatever the window.  Returns (out, lse)."""
-    import torch
-
+    torch = _torch()
     B, Hq, D = q.shape
     P, two, T, Hkv, D2 = cache.shape
     if two != 2 or D2 != D or q.dtype != cache.dtype or q.dtype not in (torch.float16, torch.bfloat16):
@@ -425,35 +427,34 @@ def decode_paged(q, cache, block_table, lengths, scale: float | None = None, kv_
     lib = load_library()
     dev = q.get_device()
     form = softcap != 0.0 or window != 0 or alibi_slopes is not None or prefix_lens is not None
-    if form:
-        slopes, prefix = _form_ptrs(alibi_slopes, prefix_lens, Hq, B, dev)
-    with _on_device(dev):
-        if kv_splits is None:
-            pick = lib.attn_decode_form_default_splits if form else lib.attn_decode_default_splits
-            kv_splits = pick(B, Hq, Hkv, T, max_pages)
-            if kv_splits < 0:
-                raise AttnError(kv_splits, "attn_decode_default_splits")
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if kv_splits is None:
+        pick = lib.attn_decode_form_default_splits if form else lib.attn_decode_default_splits
+        kv_splits = _call(dev, pick, B, Hq, Hkv, T, max_pages)
+        if kv_splits < 0:
+            raise AttnError(kv_splits, "attn_decode_default_splits")
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
         need = int(lib.attn_decode_workspace_bytes(B, Hq, D, kv_splits))
-        if workspace is None and need > 0:
+        if need > 0:
             raw = torch.empty(need + 256, dtype=torch.uint8, device=q.device)
             off = (-raw.data_ptr()) % 256
             workspace = raw[off:off + need]
-        if scale is None:
-            scale = 1.0 / math.sqrt(D)
-        sizes = (q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), out.data_ptr(),
-                 lse.data_ptr() if lse is not None else None, B, Hq, Hkv, D, T, max_pages, P, float(scale))
-        rest = (int(kv_splits), workspace.data_ptr() if workspace is not None else None,
-                (workspace.numel() if workspace is not None else 0), _raw_stream(dev, stream))
-        if form:
-            fn = lib.attn_decode_paged_form_bf16 if q.dtype == torch.bfloat16 else lib.attn_decode_paged_form
-            rc = fn(*sizes, float(softcap), int(window), slopes, prefix, *rest)
-        else:
-            fn = lib.attn_decode_paged_bf16 if q.dtype == torch.bfloat16 else lib.attn_decode_paged
-            rc = fn(*sizes, *rest)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    sizes = (q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), out.data_ptr(),
+             lse.data_ptr() if lse is not None else None, B, Hq, Hkv, D, T, max_pages, P, float(scale))
+    rest = (int(kv_splits), workspace.data_ptr() if workspace is not None else None,
+            (workspace.numel() if workspace is not None else 0), _raw_stream(dev, stream))
+    if form:
+        slopes, prefix = _form_ptrs(alibi_slopes, prefix_lens, Hq, B, dev)
+        fn = lib.attn_decode_paged_form_bf16 if q.dtype == torch.bfloat16 else lib.attn_decode_paged_form
+        rc = _call(dev, fn, *sizes, float(softcap), int(window), slopes, prefix, *rest)
+    else:
+        fn = lib.attn_decode_paged_bf16 if q.dtype == torch.bfloat16 else lib.attn_decode_paged
+        rc = _call(dev, fn, *sizes, *rest)
     if rc != 0:
         raise AttnError(rc, "attn_decode_paged")
     return out, lse
@@ -472,13 +473,9 @@ def prefill_paged(q, cache, block_table, lengths, q_offsets, scale: float | None
     [B+1] int32) the last of its lengths[b] tokens; causal; score forms as in decode_paged
     (prefix_lens tokens are visible to every row, earlier ones too).  Rows past q_offsets[B] are
     left alone.  Returns (out, lse [total,Hq] float32)."""
-    import torch
-
+    torch = _torch()
     total, Hq, D = q.shape
-    B = lengths.shape[0]
-    P, T, Hkv, D2, max_pages = _check_cache(cache, block_table, lengths, B)
-    dev = cache.get_device()
-    dt = cache.dtype
+    P, T, Hkv, D2, B, max_pages, dt, dev = _check_cache(torch, cache, block_table, lengths)
     if D2 != D:
         raise ValueError("q and cache must have the same head size")
     _check_like("q", q, (total, Hq, D), dt, dev)
@@ -496,11 +493,10 @@ def prefill_paged(q, cache, block_table, lengths, q_offsets, scale: float | None
     need = 0 if workspace is not None else lib.attn_prefill_workspace_bytes(total, B, Hq, Hkv, D, T, max_pages)
     ws, ws_bytes, held = _workspace(workspace, need, dev)
     fn = lib.attn_prefill_paged_bf16 if dt == torch.bfloat16 else lib.attn_prefill_paged
-    with _on_device(dev):
-        rc = fn(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), q_offsets.data_ptr(),
-                out.data_ptr(), lse.data_ptr(), total, B, Hq, Hkv, D, T, max_pages, P,
-                1.0 / math.sqrt(D) if scale is None else float(scale), float(softcap), int(window), slopes, prefix,
-                ws, ws_bytes, _raw_stream(dev, stream))
+    rc = _call(dev, fn, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(),
+               q_offsets.data_ptr(), out.data_ptr(), lse.data_ptr(), total, B, Hq, Hkv, D, T, max_pages, P,
+               1.0 / math.sqrt(D) if scale is None else float(scale), float(softcap), int(window), slopes, prefix,
+               ws, ws_bytes, _raw_stream(dev, stream))
     if rc != 0:
         raise AttnError(rc, "attn_prefill_paged")
     return out, lse
@@ -509,18 +505,14 @@ def prefill_paged(q, cache, block_table, lengths, q_offsets, scale: float | None
 def paged_append_chunk(new_kv, cache, block_table, lengths, q_offsets, stream=None) -> None:
     """Write new_kv [total, 2, Hkv, D], a ragged chunk packed as for prefill_paged, to the last
     positions of every request: its i-th row to lengths[b] - n_b + i."""
-    import torch
-
-    B = lengths.shape[0]
-    P, T, Hkv, D, max_pages = _check_cache(cache, block_table, lengths, B)
-    dev = cache.get_device()
+    torch = _torch()
+    P, T, Hkv, D, B, max_pages, dt, dev = _check_cache(torch, cache, block_table, lengths)
     total = new_kv.shape[0]
-    _check_like("new_kv", new_kv, (total, 2, Hkv, D), cache.dtype, dev)
+    _check_like("new_kv", new_kv, (total, 2, Hkv, D), dt, dev)
     _check_like("q_offsets", q_offsets, (B + 1,), torch.int32, dev)
-    with _on_device(dev):
-        rc = load_library().attn_paged_append_chunk(
-            new_kv.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), q_offsets.data_ptr(),
-            total, B, Hkv, D, T, max_pages, P, _raw_stream(dev, stream))
+    rc = _call(dev, load_library().attn_paged_append_chunk, new_kv.data_ptr(), cache.data_ptr(),
+               block_table.data_ptr(), lengths.data_ptr(), q_offsets.data_ptr(), total, B, Hkv, D, T, max_pages, P,
+               _raw_stream(dev, stream))
     if rc != 0:
         raise AttnError(rc, "attn_paged_append_chunk")
 
@@ -532,13 +524,9 @@ def paged_attn_mass(q, lse, cache, block_table, lengths, q_offsets=None, mass=No
     [total,Hq] came from prefill_paged or decode_paged with the same score form: summed over the
     rows and the query heads of each key/value head.  Added to ``mass`` [B,Hkv,max_pages*T] float32
     when given, else written to a new one.  Returns mass."""
-    import torch
-
+    torch = _torch()
     total, Hq, D = q.shape
-    B = lengths.shape[0]
-    P, T, Hkv, D2, max_pages = _check_cache(cache, block_table, lengths, B)
-    dev = cache.get_device()
-    dt = cache.dtype
+    P, T, Hkv, D2, B, max_pages, dt, dev = _check_cache(torch, cache, block_table, lengths)
     if D2 != D:
         raise ValueError("q and cache must have the same head size")
     _check_like("q", q, (total, Hq, D), dt, dev)
@@ -557,11 +545,10 @@ def paged_attn_mass(q, lse, cache, block_table, lengths, q_offsets=None, mass=No
         mass = torch.empty((B, Hkv, max_pages * T), dtype=torch.float32, device=q.device)
     lib = load_library()
     fn = lib.attn_paged_mass_bf16 if dt == torch.bfloat16 else lib.attn_paged_mass
-    with _on_device(dev):
-        rc = fn(q.data_ptr(), lse.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), offsets,
-                mass.data_ptr(), int(accumulate), total, B, Hq, Hkv, D, T, max_pages, P,
-                1.0 / math.sqrt(D) if scale is None else float(scale), float(softcap), int(window), slopes, prefix,
-                _raw_stream(dev, stream))
+    rc = _call(dev, fn, q.data_ptr(), lse.data_ptr(), cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(),
+               offsets, mass.data_ptr(), int(accumulate), total, B, Hq, Hkv, D, T, max_pages, P,
+               1.0 / math.sqrt(D) if scale is None else float(scale), float(softcap), int(window), slopes, prefix,
+               _raw_stream(dev, stream))
     if rc != 0:
         raise AttnError(rc, "attn_paged_mass")
     return mass
@@ -574,11 +561,8 @@ def paged_evict(cache, block_table, lengths, mass, budget: int, recent: int = 0,
     [B,Hkv,max_pages*T] float32 (ties: the lowest position).  Their rows move in place to positions
     0 .. budget - 1, in order.  Returns (kept [B,Hkv,budget] int32: each one's old position, then
     -1; new_lengths [B] int32; mass_out: the kept tokens' mass, then 0)."""
-    import torch
-
-    B = lengths.shape[0]
-    P, T, Hkv, D, max_pages = _check_cache(cache, block_table, lengths, B)
-    dev = cache.get_device()
+    torch = _torch()
+    P, T, Hkv, D, B, max_pages, _, dev = _check_cache(torch, cache, block_table, lengths)
     _check_like("mass", mass, (B, Hkv, max_pages * T), torch.float32, dev)
     budget = int(budget)
     if kept is None:
@@ -593,11 +577,9 @@ def paged_evict(cache, block_table, lengths, mass, budget: int, recent: int = 0,
         mass_out = torch.empty_like(mass)
     else:
         _check_like("mass_out", mass_out, (B, Hkv, max_pages * T), torch.float32, dev)
-    with _on_device(dev):
-        rc = load_library().attn_paged_evict(
-            cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), mass.data_ptr(), kept.data_ptr(),
-            new_lengths.data_ptr(), mass_out.data_ptr(), B, Hkv, D, T, max_pages, P, budget, int(recent),
-            _raw_stream(dev, stream))
+    rc = _call(dev, load_library().attn_paged_evict, cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(),
+               mass.data_ptr(), kept.data_ptr(), new_lengths.data_ptr(), mass_out.data_ptr(), B, Hkv, D, T, max_pages,
+               P, budget, int(recent), _raw_stream(dev, stream))
     if rc != 0:
         raise AttnError(rc, "attn_paged_evict")
     return kept, new_lengths, mass_out
