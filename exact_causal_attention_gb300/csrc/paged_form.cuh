@@ -26,8 +26,8 @@ struct CapScale {
   float out;        // cap unit
   float wide;       // 2 log2e scale / cap
   float near, far;  // |x| up to which the shorter and the longer polynomial hold
-  // Their coefficients for x^2, with the scales folded in, for pairs of scores.
-  float2 n[6], f[8];
+  float2 in;        // scale / cap, for pairs of scores
+  float2 n[6], f[8];  // their coefficients for y^2, times scale unit (powers of `in` folded in would underflow)
 };
 
 __device__ __forceinline__ CapScale cap_scale(float scale, float softcap, float unit) {
@@ -37,16 +37,16 @@ __device__ __forceinline__ CapScale cap_scale(float scale, float softcap, float 
                                  0.020557173f, -0.0067961547f, 0.0015881141f, -0.00018259805f};
   CapScale r;
   const float in = softcap > 0.f ? scale / softcap : 0.f;
+  r.in = make_float2(in, in);
   r.out = softcap * unit;
   r.wide = 2.f * kLog2e * in;
   r.near = in > 0.f ? kNear / in : 0.f;
   r.far = in > 0.f ? kFar / in : 0.f;
-  float f = scale * unit;
+  const float f = scale * unit;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (i < 6) r.n[i] = make_float2(kNearCoef[i] * f, kNearCoef[i] * f);
     r.f[i] = make_float2(kFarCoef[i] * f, kFarCoef[i] * f);
-    f *= in * in;
   }
   return r;
 }
@@ -78,7 +78,8 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k,
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const float2 x = make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-      const float2 z = __fmul2_rn(x, x);
+      const float2 y = __fmul2_rn(x, k.in);
+      const float2 z = __fmul2_rn(y, y);
       float2 a = c[kTerms - 1];
 #pragma unroll
       for (int j = kTerms - 2; j >= 0; --j) a = __ffma2_rn(a, z, c[j]);

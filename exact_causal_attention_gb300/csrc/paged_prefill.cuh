@@ -44,6 +44,8 @@ constexpr int kPfTile = 128;          // keys per tile, and rows per query tile
 constexpr int kPfUnitCost = 3;
 constexpr int kPfMinCost = 3;
 constexpr int kPfMinPart = 2;         // a unit is not cut within so many tiles of its ends
+// bf16 has fp32's exponent range: p up to 2^64 keeps l and o (at most 2^31 of them) in it.
+constexpr float kCapLead = 64.f;
 constexpr int kPfQueue = 4;
 constexpr int kPfReaders = 11;
 // Per key tile, which of its pages have a bad id.  A softmax warp reads tile j's entry
@@ -702,21 +704,28 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (lane == 0) mbar_arrive(bar(b + t));
         };
         bool move = j == first;  // take the row's max as the reference
-        if (FORM == kFormPlain && j > first && !masked) {
+        // Before every row's position a distance bias is linear in the key: slope (key - position).
+        const bool linear = FORM != kFormBias || __all_sync(0xffffffffu, ce >= kPfTile || !row_ok) != 0;
+        if ((FORM == kFormPlain || FORM == kFormBias) && j > first && !masked && linear) {
           // One pass against the reference as it stands.  Keys 64-127 load while keys 0-63 are
           // exponentiated; the checks that let a stale reference stand are those of the dense kernel.
           uint32_t s[4][32];
           uint32_t pk[2][32];
+          // What is added to a score of the tile's key 0: the reference, and its bias.
+          const float neg_at0 = FORM == kFormBias ? fmaf(-slope2, static_cast<float>(pos - kb), -m_ref) : -m_ref;
           auto exp_quarters = [&](int q0, int q1) -> float {
             float2 acc[8];
 #pragma unroll
             for (int a = 0; a < 8; ++a) acc[a] = make_float2(0.f, 0.f);
-            const float2 c2 = make_float2(c, c);
-            const float2 nm2 = make_float2(-m_ref, -m_ref);
+            const float2 c2 = make_float2(p.scale_log2e, p.scale_log2e);
+            const float2 sl2 = make_float2(slope2, slope2);
+            const float2 at0 = make_float2(neg_at0, neg_at0);
 #pragma unroll
             for (int q = q0; q < q1; ++q) {
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
+                const float2 key = make_float2(static_cast<float>(32 * q + i), static_cast<float>(32 * q + i + 1));
+                const float2 nm2 = FORM == kFormBias ? __ffma2_rn(sl2, key, at0) : at0;
                 const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), c2, nm2);
                 const float2 e = make_float2(ex2(x.x), ex2(x.y));
                 acc[(i / 2) % 8] = __fadd2_rn(acc[(i / 2) % 8], e);
@@ -740,7 +749,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             mx[0] = fmax3(mx[0], __uint_as_float(s[2][i]), __uint_as_float(s[2][i + 1]));
             mx[1] = fmax3(mx[1], __uint_as_float(s[3][i]), __uint_as_float(s[3][i + 1]));
           }
-          const float top_b = fmaxf(mx[0], mx[1]) * c - m_ref;
+          // (with a bias, at most that of key 127, or 64 should the slope be negative)
+          const float top_b = fmaf(fmaxf(mx[0], mx[1]), p.scale_log2e,
+                                   FORM == kFormBias ? fmaf(slope2, slope2 >= 0.f ? 127.f : 64.f, neg_at0) : -m_ref);
           const bool fast = !row_ok || (sum_a <= max_row_sum<BF16>() && top_b <= max_lead<BF16>());
           if (__all_sync(0xffffffffu, fast)) {
             tmem_st_x32(t_s, pk[0]);
@@ -752,6 +763,40 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             continue;
           }
           move = !fast;  // S is still intact in TMEM: P has not been stored yet
+        }
+        if constexpr (FORM == kFormCap && BF16) {
+          // No score exceeds the cap: where that is near enough to the reference for bf16's range, no check
+          // is needed and one pass does.
+          if (j > first && !masked && __all_sync(0xffffffffu, !row_ok || cap.out - m_ref <= kCapLead)) {
+            const float2 nm2 = make_float2(-m_ref, -m_ref);
+            float2 acc[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) acc[a] = make_float2(0.f, 0.f);
+            uint32_t next[32];
+            tmem_ld_x32(t_s, next);
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t s[32], pk[16];
+              tmem_wait_ld_x32(next);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[i] = next[i];
+              if (q < 3) tmem_ld_x32(t_s + 32u * (q + 1), next);
+              cap_scores<false, false>(s, cap, nullptr);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 x = __fadd2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), nm2);
+                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                acc[(i / 2) % 4] = __fadd2_rn(acc[(i / 2) % 4], e);
+                pk[i / 2] = pack2<BF16>(e.x, e.y);
+              }
+              // P of this quarter over scores that have been read.
+              tmem_st_x16(t_s + 16u * q, pk);
+              if (q & 1) hand_over(q == 1 ? L::kBarPa : L::kBarPb);
+            }
+            const float2 both = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+            l += both.x + both.y;
+            continue;
+          }
         }
         // Two passes: the first applies the form and the mask, takes the row's max and writes the scores
         // back, the second exponentiates them against a reference that is known to hold.  (The first

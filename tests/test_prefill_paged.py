@@ -28,6 +28,10 @@ CASES = {
     "small_cap": (4, 4, 64, 16, [(20, 150)], "fp16", dict(softcap=2.0, q_std=3.0)),
     "alibi": (8, 8, 64, 16, [(140, 300), (1, 200)], "fp16", dict(slopes=ALIBI)),
     "alibi_grouped_prefix": (8, 2, 128, 16, [(40, 170), (64, 64)], "bf16", dict(slopes=ALIBI, prefix=[30, 64])),
+    "alibi_negative": (4, 2, 64, 16, [(40, 700), (300, 300)], "fp16", dict(slopes="away")),
+    "cap_fp16_long": (8, 2, 128, 16, [(40, 1200)], "fp16", dict(softcap=30.0, q_std=8.0)),
+    "cap_bf16_long": (8, 2, 128, 16, [(40, 1200), (130, 600)], "bf16", dict(softcap=50.0, q_std=8.0)),
+    "cap_bf16_low_start": (4, 2, 64, 16, [(150, 900)], "bf16", dict(softcap=70.0, q_std=20.0)),
     "window": (8, 2, 128, 16, [(50, 700), (1, 500), (129, 129)], "fp16", dict(window=100)),
     "window_1": (4, 2, 64, 16, [(5, 40), (130, 130)], "fp16", dict(window=1)),
     "window_tile_edge": (4, 1, 64, 32, [(256, 640)], "bf16", dict(window=128)),
@@ -38,13 +42,19 @@ CASES = {
 }
 
 
+def slopes_of(kind, Hq):
+    """ALIBI: 2^(-8 (h + 1) / Hq); "away": negative, weight that grows with the distance."""
+    h = torch.arange(1, Hq + 1, dtype=torch.float32)
+    return torch.exp2(-8.0 * h / Hq) if kind == ALIBI else -0.05 * h
+
+
 def case_inputs(name, spare_rows=0):
     Hq, Hkv, D, T, sizes, dtype, form = CASES[name]
     form = dict(form)
     q, cache, table, lens, offsets = ref.chunk(len(sizes), Hq, Hkv, D, T, sizes, dtype, 1000 + len(name) * 7 + D,
                                                form.pop("q_std", 1.0), spare_rows)
-    if form.get("slopes") == ALIBI:
-        form["slopes"] = torch.exp2(-8.0 * torch.arange(1, Hq + 1, dtype=torch.float32) / Hq)
+    if "slopes" in form:
+        form["slopes"] = slopes_of(form["slopes"], Hq)
     if "prefix" in form:
         form["prefix"] = torch.tensor(form["prefix"], dtype=torch.int32)
     return q, cache, table, lens, offsets, dtype, T, form
@@ -97,7 +107,7 @@ def test_decode_with_score_forms_matches_the_definition(cuda_lib, name, splits):
     q, cache, table, lens, offsets = ref.chunk(len(sizes), Hq, Hkv, D, T, sizes, dtype, 77 + len(name),
                                                form.pop("q_std", 1.0))
     if "slopes" in form:
-        form["slopes"] = torch.exp2(-8.0 * torch.arange(1, Hq + 1, dtype=torch.float32) / Hq)
+        form["slopes"] = slopes_of(form["slopes"], Hq)
     if "prefix" in form:
         form["prefix"] = torch.tensor([*form["prefix"], 3, 1, 40], dtype=torch.int32)
     o, l, tol_o, tol_l = ref.attention(q, cache, table, lens, offsets, T, dtype, 1.0 / math.sqrt(D), **form)
