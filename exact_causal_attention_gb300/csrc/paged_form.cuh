@@ -21,13 +21,16 @@ constexpr int kFormBoth = 3;  // cap, then bias
 __host__ __device__ constexpr bool form_caps(int form) { return form == kFormCap || form == kFormBoth; }
 __host__ __device__ constexpr bool form_biases(int form) { return form == kFormBias || form == kFormBoth; }
 
-// Scales of the cap: cap_scores gives unit * cap tanh(x scale / cap).
+// Scales of the cap: cap_scores gives big * unit * cap tanh(x scale / cap).  The polynomials run in
+// x^2, with powers of scale / cap folded into their coefficients; `big`, a power of two of about
+// (cap / scale)^7, keeps the highest coefficient from underflowing, and goes out again with a
+// multiplication that the caller does anyway.
 struct CapScale {
   float out;        // cap unit
+  float big, inv_big;
   float wide;       // 2 log2e scale / cap
   float near, far;  // |x| up to which the shorter and the longer polynomial hold
-  float2 in;        // scale / cap, for pairs of scores
-  float2 n[6], f[8];  // their coefficients for y^2, times scale unit (powers of `in` folded in would underflow)
+  float2 n[6], f[8];  // their coefficients for x^2, for pairs of scores
 };
 
 __device__ __forceinline__ CapScale cap_scale(float scale, float softcap, float unit) {
@@ -37,33 +40,38 @@ __device__ __forceinline__ CapScale cap_scale(float scale, float softcap, float 
                                  0.020557173f, -0.0067961547f, 0.0015881141f, -0.00018259805f};
   CapScale r;
   const float in = softcap > 0.f ? scale / softcap : 0.f;
-  r.in = make_float2(in, in);
   r.out = softcap * unit;
+  // Outside 2^-12 .. 2^12 the coefficients would leave the type.  Below, the low terms alone reach as far
+  // as 0.05; above, an error of 3e-7 of the cap is below a score's own rounding.
+  const bool low = in < 0x1p-12f, high = in > 0x1p12f;
+  r.big = low || high ? 1.f : exp2f(rintf(-7.f * log2f(in)));
+  r.inv_big = 1.f / r.big;
   r.wide = 2.f * kLog2e * in;
-  r.near = in > 0.f ? kNear / in : 0.f;
-  r.far = in > 0.f ? kFar / in : 0.f;
-  const float f = scale * unit;
+  r.near = high ? -1.f : (low ? fminf(0.05f / in, 1e18f) : kNear / in);
+  r.far = high ? -1.f : (low ? r.near : kFar / in);
+  float f = scale * unit * r.big;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (i < 6) r.n[i] = make_float2(kNearCoef[i] * f, kNearCoef[i] * f);
     r.f[i] = make_float2(kFarCoef[i] * f, kFarCoef[i] * f);
+    f *= in * in;
   }
   return r;
 }
 
-// out tanh(x in) + plus by tanh(y) = 1 - 2 / (1 + e^2y), for x that is not small.  `plus` joins the
+// big out tanh(x in) + plus by tanh(y) = 1 - 2 / (1 + e^2y), for x that is not small.  `plus` joins the
 // leading term, so that where the sum is small its rounding is too.
 __device__ __forceinline__ float cap_wide(float x, const CapScale& k, float plus) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(fabsf(x) * k.wide) + 1.f));
-  const float side = copysignf(k.out, x);
+  const float side = copysignf(k.out * k.big, x);
   return fmaf(-2.f * side, r, side + plus);
 }
 
-// A whole warp: 32 scores per thread, x to unit cap tanh(x scale / cap), plus add[i] where
+// A whole warp: 32 scores per thread, x to big unit cap tanh(x scale / cap), plus add[i] where
 // there is one (in shared memory, 16-byte aligned, the same for every thread).  kNear: with
 // the shorter polynomial, and the longer one in mixed groups too; a kernel whose warps wait for
-// instructions does better without (a mixed step's chunk attention: 209 us, with them 227).
+// instructions does better without (a mixed step: chunk attention 209 us, with them 227).
 template <bool kAdd, bool kNear>
 __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k, const float* add) {
   float m4[4] = {0.f, 0.f, 0.f, 0.f};
@@ -78,8 +86,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[32], const CapScale& k,
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const float2 x = make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-      const float2 y = __fmul2_rn(x, k.in);
-      const float2 z = __fmul2_rn(y, y);
+      const float2 z = __fmul2_rn(x, x);
       float2 a = c[kTerms - 1];
 #pragma unroll
       for (int j = kTerms - 2; j >= 0; --j) a = __ffma2_rn(a, z, c[j]);

@@ -421,6 +421,8 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
     }
   } else if (warp == kColumns) {
     // ------------------------------------------------- the columns' values, lane by column
+    // (times the power of two that capped scores come with)
+    const float big = form_caps(FORM) ? cap_scale(p.f.scale, p.f.softcap, 1.f).big : 1.f;
     int tok[4], head[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
           next[c] = -INFINITY;
           if (tok[c] < p.tq && t0 + tok[c] < w.n) {
             const float z = p.lse[static_cast<size_t>(w.row0 + t0 + tok[c]) * p.Hq + (w.kvh * p.chunks + chunk) * p.hc + head[c]];
-            next[c] = z == -INFINITY ? z : -z;
+            next[c] = z == -INFINITY ? z : -z * big;
           }
         }
       };
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
         for (int c = 0; c < 4; ++c) {
           dst[lane + 32 * c] = now[c];
           if constexpr (form_biases(FORM)) {
-            dst[kMsCols + lane + 32 * c] = p.f.slopes[(w.kvh * p.chunks + chunk) * p.hc + head[c]];
+            dst[kMsCols + lane + 32 * c] = big * p.f.slopes[(w.kvh * p.chunks + chunk) * p.hc + head[c]];
             dst[2 * kMsCols + lane + 32 * c] = static_cast<float>(w.pos0 + t0 + tok[c]);
           }
         }
@@ -479,6 +481,7 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
     const int log2T = 31 - __clz(p.s.page_size);
     auto warp_wait = [&](uint32_t b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, wd.wait(b, ph)) != 0; };
     const CapScale cap = cap_scale(p.f.scale, p.f.softcap, 1.f);
+    const float to_base2 = form_caps(FORM) ? kLog2e * cap.inv_big : kLog2e;
     float* sums_s = reinterpret_cast<float*>(smem + L::kSumOff) + 2 * x * kMsTile;
     int it = 0, step = 0, uses = 0;
     int joined = 0;  // units of this slot whose halves were joined
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(kMsThreads<kParts>, 1)
         // Sums 32 columns: 2^(log2e (form(s) - lse)).
         auto add = [&](uint32_t (&v)[32], int q) {
           if constexpr (form_caps(FORM)) cap_scores<true, true>(v, cap, col + 32 * q);
-          const float2 c2 = make_float2(p.f.scale, p.f.scale), k2 = make_float2(kLog2e, kLog2e);
+          const float2 c2 = make_float2(p.f.scale, p.f.scale), k2 = make_float2(to_base2, to_base2);
           const bool all = __all_sync(0xffffffffu, lo <= 32 * q && hi >= 32 * q + 32) != 0;
           auto low = [](int m) -> uint32_t { return m <= 0 ? 0u : (m >= 32 ? ~0u : (1u << m) - 1u); };
           const uint32_t seen = low(hi - 32 * q) & ~low(lo - 32 * q);

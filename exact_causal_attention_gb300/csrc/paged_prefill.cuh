@@ -44,8 +44,6 @@ constexpr int kPfTile = 128;          // keys per tile, and rows per query tile
 constexpr int kPfUnitCost = 3;
 constexpr int kPfMinCost = 3;
 constexpr int kPfMinPart = 2;         // a unit is not cut within so many tiles of its ends
-// bf16 has fp32's exponent range: p up to 2^64 keeps l and o (at most 2^31 of them) in it.
-constexpr float kCapLead = 64.f;
 constexpr int kPfQueue = 4;
 constexpr int kPfReaders = 11;
 // Per key tile, which of its pages have a bad id.  A softmax warp reads tile j's entry
@@ -602,9 +600,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t t_s = tmem + lane_base + 128u * t;
     const uint32_t t_o = tmem + lane_base + 256u + static_cast<uint32_t>(D) * t;
-    // Scores arrive as q . k; the form turns them into the base-2 domain.
-    const float c = FORM == kFormPlain ? p.scale_log2e : 1.f;
+    // Scores arrive as q . k; the form's pass leaves them in the base-2 domain but for a factor c.
     const CapScale cap = cap_scale(p.f.scale, p.f.softcap, kLog2e);
+    const float c = FORM == kFormPlain ? p.scale_log2e : (FORM == kFormCap ? cap.inv_big : 1.f);
     const int row_tok = fast_div(r_local, p.by_hc);  // this row's token and head within the tile
     const int row_head = r_local - row_tok * p.hc;
     const int T = p.s.page_size;
@@ -764,40 +762,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
           move = !fast;  // S is still intact in TMEM: P has not been stored yet
         }
-        if constexpr (FORM == kFormCap && BF16) {
-          // No score exceeds the cap: where that is near enough to the reference for bf16's range, no check
-          // is needed and one pass does.
-          if (j > first && !masked && __all_sync(0xffffffffu, !row_ok || cap.out - m_ref <= kCapLead)) {
-            const float2 nm2 = make_float2(-m_ref, -m_ref);
-            float2 acc[4];
-#pragma unroll
-            for (int a = 0; a < 4; ++a) acc[a] = make_float2(0.f, 0.f);
-            uint32_t next[32];
-            tmem_ld_x32(t_s, next);
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              uint32_t s[32], pk[16];
-              tmem_wait_ld_x32(next);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] = next[i];
-              if (q < 3) tmem_ld_x32(t_s + 32u * (q + 1), next);
-              cap_scores<false, false>(s, cap, nullptr);
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 x = __fadd2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), nm2);
-                const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                acc[(i / 2) % 4] = __fadd2_rn(acc[(i / 2) % 4], e);
-                pk[i / 2] = pack2<BF16>(e.x, e.y);
-              }
-              // P of this quarter over scores that have been read.
-              tmem_st_x16(t_s + 16u * q, pk);
-              if (q & 1) hand_over(q == 1 ? L::kBarPa : L::kBarPb);
-            }
-            const float2 both = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-            l += both.x + both.y;
-            continue;
-          }
-        }
         // Two passes: the first applies the form and the mask, takes the row's max and writes the scores
         // back, the second exponentiates them against a reference that is known to hold.  (The first
         // is a loop: with the form's code inlined four times and more the softmax warps waited for
@@ -813,7 +777,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const float away = static_cast<float>(pos - kb - 32 * q);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float x = FORM == kFormBias ? __uint_as_float(s[i]) * p.scale_log2e : __uint_as_float(s[i]);
+              const float x = __uint_as_float(s[i]) * (FORM == kFormBias ? p.scale_log2e : cap.inv_big);
               s[i] = __float_as_uint(fmaf(-slope2, fabsf(away - static_cast<float>(i)), x));
             }
           }

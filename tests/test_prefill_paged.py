@@ -31,6 +31,8 @@ CASES = {
     "alibi_negative": (4, 2, 64, 16, [(40, 700), (300, 300)], "fp16", dict(slopes="away")),
     "cap_fp16_long": (8, 2, 128, 16, [(40, 1200)], "fp16", dict(softcap=30.0, q_std=8.0)),
     "cap_bf16_long": (8, 2, 128, 16, [(40, 1200), (130, 600)], "bf16", dict(softcap=50.0, q_std=8.0)),
+    "cap_vast": (4, 2, 64, 16, [(40, 300)], "fp16", dict(softcap=5000.0, q_std=8.0)),
+    "cap_tiny": (4, 2, 64, 16, [(40, 300)], "fp16", dict(softcap=1e-5)),
     "cap_bf16_low_start": (4, 2, 64, 16, [(150, 900)], "bf16", dict(softcap=70.0, q_std=20.0)),
     "window": (8, 2, 128, 16, [(50, 700), (1, 500), (129, 129)], "fp16", dict(window=100)),
     "window_1": (4, 2, 64, 16, [(5, 40), (130, 130)], "fp16", dict(window=1)),
