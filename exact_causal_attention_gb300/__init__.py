@@ -405,6 +405,16 @@ def _call(dev: int, fn, *args) -> int:
         return fn(*args)
 
 
+def _within(stream, dev: int):
+    """``stream`` as torch's current one: what is allocated inside belongs to it, so that work still
+    queued on another stream cannot reach the same memory."""
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
 def decode_paged(q, cache, block_table, lengths, scale: float | None = None, kv_splits: int | None = None,
                  out=None, lse=None, workspace=None, stream=None, softcap: float = 0.0, alibi_slopes=None,
                  window: int = 0, prefix_lens=None):
@@ -423,9 +433,13 @@ def decode_paged(q, cache, block_table, lengths, scale: float | None = None, kv_
     for t in (q, cache, block_table, lengths):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("all tensors must be contiguous CUDA tensors")
+    dev = q.get_device()
+    if stream is not None and (out is None or lse is None or workspace is None):
+        with _within(stream, dev):
+            return decode_paged(q, cache, block_table, lengths, scale, kv_splits, out, lse, workspace, None, softcap,
+                                alibi_slopes, window, prefix_lens)
     max_pages = block_table.shape[1]
     lib = load_library()
-    dev = q.get_device()
     form = softcap != 0.0 or window != 0 or alibi_slopes is not None or prefix_lens is not None
     if kv_splits is None:
         pick = lib.attn_decode_form_default_splits if form else lib.attn_decode_default_splits
@@ -481,6 +495,10 @@ def prefill_paged(q, cache, block_table, lengths, q_offsets, scale: float | None
     _check_like("q", q, (total, Hq, D), dt, dev)
     _check_like("q_offsets", q_offsets, (B + 1,), torch.int32, dev)
     slopes, prefix = _form_ptrs(alibi_slopes, prefix_lens, Hq, B, dev)
+    if stream is not None and (out is None or lse is None or workspace is None):
+        with _within(stream, dev):
+            return prefill_paged(q, cache, block_table, lengths, q_offsets, scale, softcap, alibi_slopes, window,
+                                 prefix_lens, out, lse, workspace)
     if out is None:
         out = torch.empty_like(q)
     else:
@@ -539,6 +557,10 @@ def paged_attn_mass(q, lse, cache, block_table, lengths, q_offsets=None, mass=No
         raise ValueError("without q_offsets q holds one row a request")
     slopes, prefix = _form_ptrs(alibi_slopes, prefix_lens, Hq, B, dev)
     accumulate = mass is not None
+    if stream is not None and not accumulate:
+        with _within(stream, dev):
+            return paged_attn_mass(q, lse, cache, block_table, lengths, q_offsets, None, scale, softcap, alibi_slopes,
+                                   window, prefix_lens)
     if accumulate:
         _check_like("mass", mass, (B, Hkv, max_pages * T), torch.float32, dev)
     else:
@@ -565,6 +587,9 @@ def paged_evict(cache, block_table, lengths, mass, budget: int, recent: int = 0,
     P, T, Hkv, D, B, max_pages, _, dev = _check_cache(torch, cache, block_table, lengths)
     _check_like("mass", mass, (B, Hkv, max_pages * T), torch.float32, dev)
     budget = int(budget)
+    if stream is not None and (kept is None or new_lengths is None or mass_out is None):
+        with _within(stream, dev):
+            return paged_evict(cache, block_table, lengths, mass, budget, recent, kept, new_lengths, mass_out)
     if kept is None:
         kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=cache.device)
     else:

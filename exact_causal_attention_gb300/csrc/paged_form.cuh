@@ -5,7 +5,8 @@
 // mostly well inside the cap, where tanh(y) = y P(y^2) takes multiply-adds alone: P is a
 // polynomial fitted to tanh(y) / y by iteratively reweighted least squares, of degree 5 on
 // |y| <= 0.75 or 7 on |y| <= 1.25 (relative errors 3e-8 and 8e-8 before rounding).  In a group of
-// scores with some outside those take the exponential.
+// scores with some outside those take the exponential.  (Weights of 500 tokens over 12000 keys, two requests: 154 us with
+// a cap of 50, 253 with 20, where most groups have some outside.)
 #pragma once
 #include <type_traits>
 

@@ -325,6 +325,49 @@ def test_append_attend_weigh_evict_and_go_on(cuda_lib, captured):
 
 # ---------------------------------------------------------------- refusals, without a GPU
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", ["prefill", "decode", "decode_form", "mass", "evict"])
+def test_results_allocated_for_another_stream(cuda_lib, op):
+    """With stream= given, results and workspaces belong to that stream: a write still queued on the
+    current stream, to a block that was freed since, does not reach them."""
+    eca = cuda_lib
+    B, Hq, Hkv, D, T, pages = 2, 8, 2, 64, 16, 64
+    g = torch.Generator().manual_seed(5)
+    lens = torch.tensor([900, 700], dtype=torch.int32).cuda()
+    cache = torch.randn((B * pages, 2, T, Hkv, D), generator=g).half().cuda()
+    table = torch.randperm(B * pages, generator=g).int().reshape(B, pages).cuda()
+    q = torch.randn((B, Hq, D), generator=g).half().cuda()
+    lse = torch.full((B, Hq), 5.0, device="cuda")
+    offsets = torch.arange(B + 1, dtype=torch.int32).cuda()
+    weights = torch.rand((B, Hkv, pages * T), generator=g).cuda()
+
+    def call(stream):
+        if op == "prefill":
+            return eca.prefill_paged(q, cache, table, lens, offsets, stream=stream)
+        if op == "decode":
+            return eca.decode_paged(q, cache, table, lens, stream=stream)
+        if op == "decode_form":
+            return eca.decode_paged(q, cache, table, lens, stream=stream, window=500)
+        if op == "mass":
+            return (eca.paged_attn_mass(q, lse, cache, table, lens, stream=stream),)
+        return eca.paged_evict(cache, table, lens, weights, 1000, 10, stream=stream)
+
+    want = [x.clone() for x in call(None)]  # (the eviction moves nothing: every request fits its budget)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        held = [torch.empty_like(x) for x in want for _ in range(3)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        for x in held:
+            x.fill_(7)
+        del held, x
+        got = call(stream)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert eca.device_status() == 0
+
+
 def test_append_chunk_refusals_without_a_gpu(lib):
     f = lib.attn_paged_append_chunk
 
